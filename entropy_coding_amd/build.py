@@ -4,6 +4,7 @@ Flags that matter for bit-exactness of the shared CDF: no floating-point
 contraction (-ffp-contract=off), float32 denormals kept
 (-fno-gpu-flush-denormals-to-zero), and no packed-fp32 instructions.
 """
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -14,6 +15,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
 ARCH = os.environ.get("KVC_OFFLOAD_ARCH", "gfx950")
+
+KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip"]
+HOST = ["kvc_api.cpp", "kvc_paged_api.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
@@ -36,22 +40,24 @@ def build(verbose: bool = False) -> str:
     cc = hipcc()
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
-    objs = []
     rocm = os.path.dirname(os.path.dirname(cc))
     host_cxx = shutil.which("g++") or "g++"
-    steps = [
-        (cc, "kvc_kernels.hip", DEVICE),
-        # the C ABI layer is host code only: plain g++ against the HIP runtime API
-        (host_cxx, "kvc_api.cpp", ["-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(rocm, "include"),
-                                   "-Wall", "-Wextra"]),
-    ]
-    for comp, src, extra in steps:
+    host = ["-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(rocm, "include"), "-Wall", "-Wextra"]
+    steps = [(cc, src, DEVICE) for src in KERNELS]
+    # the C ABI layer is host code only: plain g++ against the HIP runtime API
+    steps += [(host_cxx, src, host) for src in HOST]
+
+    def compile_one(step):
+        comp, src, extra = step
         obj = os.path.join(obj_dir, os.path.splitext(src)[0] + ".o")
         cmd = [comp, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        objs = list(pool.map(compile_one, steps))
     tmp = LIB + ".tmp"
     cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     if verbose:
@@ -66,7 +72,7 @@ CHECKED_LIB = os.path.join(CHECKED_DIR, "libkvc_checked.so")
 
 
 def build_checked(verbose: bool = False) -> str:
-    """A second build for the CPU tests only: the C ABI layer compiled with
+    """A second build for the CPU tests only: the C ABI layer (HOST) compiled with
     AddressSanitizer and UndefinedBehaviorSanitizer (g++; any finding aborts
     the process), linked with the same device code into
     _build/checked/libkvc_checked.so.  The host tests load it in a child
@@ -75,15 +81,18 @@ def build_checked(verbose: bool = False) -> str:
     cc = hipcc()
     os.makedirs(CHECKED_DIR, exist_ok=True)
     rocm = os.path.dirname(os.path.dirname(cc))
-    kern = os.path.join(HERE, "_build", "kvc_kernels.o")     # the device code of build()
-    api = os.path.join(CHECKED_DIR, "kvc_api.o")
+    obj = lambda where, src: os.path.join(where, os.path.splitext(src)[0] + ".o")
+    kern = {src: obj(os.path.join(HERE, "_build"), src) for src in KERNELS}     # the device code of build()
+    api = {src: obj(CHECKED_DIR, src) for src in HOST}
     host_cxx = shutil.which("g++") or "g++"
     san = ["-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-fno-omit-frame-pointer", "-g"]
-    cmds = [] if os.path.exists(kern) else [[cc, *COMMON, *DEVICE, "-c", os.path.join(CSRC, "kvc_kernels.hip"), "-o", kern]]
+    cmds = [[cc, *COMMON, *DEVICE, "-c", os.path.join(CSRC, src), "-o", o]
+            for src, o in kern.items() if not os.path.exists(o)]
+    cmds += [[host_cxx, *[f for f in COMMON if f != "-O3"], "-O1", *san, "-D__HIP_PLATFORM_AMD__",
+              "-I" + os.path.join(rocm, "include"), "-Wall", "-Wextra", "-c", os.path.join(CSRC, src), "-o", o]
+             for src, o in api.items()]
     cmds += [
-        [host_cxx, *[f for f in COMMON if f != "-O3"], "-O1", *san, "-D__HIP_PLATFORM_AMD__",
-         "-I" + os.path.join(rocm, "include"), "-Wall", "-Wextra", "-c", os.path.join(CSRC, "kvc_api.cpp"), "-o", api],
-        [host_cxx, "-shared", *san, kern, api, "-o", CHECKED_LIB + ".tmp", "-L" + os.path.join(rocm, "lib"),
+        [host_cxx, "-shared", *san, *kern.values(), *api.values(), "-o", CHECKED_LIB + ".tmp", "-L" + os.path.join(rocm, "lib"),
          "-Wl,-rpath," + os.path.join(rocm, "lib"), "-lamdhip64"],
     ]
     for cmd in cmds:

@@ -1,0 +1,118 @@
+// Host-side interface between the C ABI (kvc_paged_api.cpp) and the kernels
+// of the paged cache: block tables and appends (kvc_paged.hip), attention
+// (kvc_attention.hip).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace kvc {
+
+constexpr uint32_t kPagedMagic = 0x6b766361u;      // a workspace that a call has written
+enum : uint32_t {
+    kPagedInvalid = 1u,
+    kPagedCapacity = 2u,
+};
+
+// ---- block tables
+
+// Head of the workspace; behind it (at kTableArraysOffset) three int32
+// arrays of batch + 1 entries, table_array(batch) apart: the prefix sums of
+// the pages taken, of the pages given back, and the held counts before.
+struct TableControl {
+    uint32_t magic;
+    uint32_t flags;
+    int64_t rows;
+    int32_t count;                      // height of the stack before
+    int32_t taken, given;               // pages
+    uint32_t pad;
+};
+constexpr uint64_t kTableArraysOffset = 256;
+inline __host__ __device__ int64_t table_array(int64_t batch) { return (batch + 64) & ~int64_t(15); }
+
+struct TableArgs {
+    int64_t batch, max_pages, num_pages, free_capacity, max_rows;
+    uint32_t page_tokens, trim;
+    const int32_t* cached;
+    const int32_t* fresh;
+    const int32_t* held_in;
+    int32_t* held_out;
+    int32_t* table;
+    int32_t* free_pages;
+    const int32_t* free_in;
+    int32_t* free_out;
+    int32_t* row_starts;
+    int64_t* slots;
+    int32_t* positions;
+    TableControl* ctl;
+    int32_t* arrays;
+};
+hipError_t launch_block_table(const TableArgs& a, hipStream_t s);
+
+// ---- append
+
+struct AppendArgs {
+    void* const* pools;                 // the layer's K pool, then its V pool
+    const void* k;
+    const void* v;
+    const int64_t* slots;
+    int64_t rows, n_slots;              // n_slots: num_pages x page_tokens
+    int64_t k_stride, v_stride;         // bytes
+    uint32_t row_bytes;                 // of a pool's row (heads x channels)
+    float k_scale, v_scale;
+};
+hipError_t launch_append(const AppendArgs& a, bool rounds, hipStream_t s);
+
+// ---- attention
+
+// Head of the workspace; behind it one AttendSpan a sequence, then a word a
+// workgroup (not 0: it met a page number outside the pool), then the partial
+// outputs and their (maximum, sum) pairs, each part 256-byte aligned.
+struct AttendControl {
+    uint32_t magic;
+    uint32_t flags;                     // kPagedInvalid: a sequence that does not fit
+    uint32_t grid;
+    uint32_t words_offset;
+};
+struct AttendSpan {                     // where a sequence's partials lie
+    uint32_t base;                      // its first workgroup
+    uint32_t splits;                    // 0: none of its rows is computed
+    uint32_t tiles;                     // row tiles
+    uint32_t pad;
+};
+
+struct AttendShape {                    // what the launch is made for
+    int row_tiles;                      // 16-row tiles a workgroup holds
+    uint32_t target;                    // workgroups that fill the chip
+    uint32_t grid;
+    bool split;                         // whether a sequence may be split
+    uint64_t spans, words, partial, pairs, total;   // workspace offsets and size
+};
+
+struct AttendArgs {
+    void* const* pools;                 // the layer's K pool, then its V pool
+    const int32_t* block_table;
+    int64_t max_pages, num_pages;
+    uint32_t page_tokens, heads, batch, ratio;
+    const uint16_t* q;
+    int64_t q_row, q_head;
+    uint16_t* out;
+    int64_t out_row;
+    float* lse;
+    const int32_t* row_starts;
+    const int32_t* context;
+    const uint64_t* mask;
+    uint32_t mask_words, rows;
+    float scale_log2, v_scale;
+    uint32_t target, split;
+    AttendControl* ctl;
+    AttendSpan* spans;
+    uint32_t* words;
+    float* partial;
+    float* pairs;                       // (maximum, sum) each
+};
+AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t channels, bool fp8, int64_t rows,
+                         int64_t rows_per_sequence, int64_t max_tokens);
+hipError_t launch_attend(const AttendArgs& a, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
+
+}  // namespace kvc

@@ -35,6 +35,8 @@ EXPORTS = [
     "kvc_decode_paged", "kvc_reload",
     "kvc_calibrate_sigma", "kvc_calibrate_sigma_blocks", "kvc_calibrate_sigma_rate", "kvc_calibrate_split",
     "kvc_build_marginal", "kvc_estimate_bits", "kvc_cdf_table",
+    "kvc_build_block_table", "kvc_block_table_result", "kvc_paged_append",
+    "kvc_paged_attention_sizes", "kvc_paged_attention", "kvc_paged_attention_result",
 ]
 
 if not os.path.exists(LIB_PATH):
@@ -68,6 +70,30 @@ class kvc_encode_info(ctypes.Structure):
 class kvc_decode_info(ctypes.Structure):
     _fields_ = [("stage_ms", ctypes.c_float * 2), ("reserved", ctypes.c_uint32),
                 ("fallback_symbols", ctypes.c_uint64)]
+
+
+class kvc_block_table(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+        ("free_capacity", ctypes.c_int64), ("max_rows", ctypes.c_int64),
+        ("page_tokens", ctypes.c_uint32), ("trim", ctypes.c_uint32),
+        ("d_cached_lens", ctypes.c_void_p), ("d_new_lens", ctypes.c_void_p), ("d_held_in", ctypes.c_void_p),
+        ("d_held_out", ctypes.c_void_p), ("d_block_table", ctypes.c_void_p), ("d_free_pages", ctypes.c_void_p),
+        ("d_free_in", ctypes.c_void_p), ("d_free_out", ctypes.c_void_p), ("d_row_starts", ctypes.c_void_p),
+        ("d_slots", ctypes.c_void_p), ("d_positions", ctypes.c_void_p),
+    ]
+
+
+class kvc_attention(ctypes.Structure):
+    _fields_ = [
+        ("d_q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("d_out", ctypes.c_void_p), ("out_row_stride", ctypes.c_int64), ("d_lse", ctypes.c_void_p),
+        ("d_row_starts", ctypes.c_void_p), ("d_context_lens", ctypes.c_void_p), ("d_tree_mask", ctypes.c_void_p),
+        ("mask_words", ctypes.c_int64), ("rows", ctypes.c_int64), ("rows_per_sequence", ctypes.c_int64),
+        ("max_tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("channels", ctypes.c_int64),
+        ("kv_dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+    ]
 
 
 _P = ctypes.c_void_p
@@ -116,6 +142,18 @@ _lib_calibrate_split = _sig("kvc_calibrate_split", ctypes.c_int,
 _lib_marginal = _sig("kvc_build_marginal", ctypes.c_int, [_P, _I32, _U64, _U32, _U32, _P, _P])
 _lib_estimate = _sig("kvc_estimate_bits", ctypes.c_int, [ctypes.POINTER(kvc_params), _P, _P, _P, _P, _P, _P, _U64, _P])
 _lib_cdf_table = _sig("kvc_cdf_table", ctypes.c_int, [_I32, _I32, _U32, _U32, _U32, _P, _P, _I64, _P, _P, _P])
+
+_F32 = ctypes.c_float
+_lib_block_table = _sig("kvc_build_block_table", ctypes.c_int,
+                        [ctypes.POINTER(kvc_block_table), _P, _U64, _P, ctypes.POINTER(_I64)])
+_lib_block_table_result = _sig("kvc_block_table_result", ctypes.c_int, [_P, _P, ctypes.POINTER(_I64)])
+_lib_append = _sig("kvc_paged_append", ctypes.c_int,
+                   [ctypes.POINTER(kvc_paged_kv), _I64, _I32, _I64, _P, _P, _I32, _I64, _I64, _I64, _P, _F32, _F32, _P])
+_lib_attention_sizes = _sig("kvc_paged_attention_sizes", ctypes.c_int,
+                            [ctypes.POINTER(kvc_paged_kv), ctypes.POINTER(kvc_attention), ctypes.POINTER(_U64)])
+_lib_attention = _sig("kvc_paged_attention", ctypes.c_int,
+                      [ctypes.POINTER(kvc_paged_kv), _I64, ctypes.POINTER(kvc_attention), _P, _U64, _P])
+_lib_attention_result = _sig("kvc_paged_attention_result", ctypes.c_int, [_P, _P])
 
 
 class KvcError(RuntimeError):
@@ -450,6 +488,8 @@ class PagedKV:
         self.dtype = pools[0].dtype
         self.desc = kvc_paged_kv(self.ptrs.data_ptr(), block_table.data_ptr(), len(pools), _nbytes(pools[0]),
                                  block_table.shape[0], heads, block_table.shape[1], n_pages, page_tokens, 0)
+        self.kv_dtype = _kv_dtype(pools[0])
+        self.ref = ctypes.byref(self.desc)
 
 
 def kvc_decode_paged(stream_bytes, mu, sigma, prefix, paged: PagedKV, workspace, stream=None,
@@ -471,6 +511,203 @@ def kvc_decode_paged(stream_bytes, mu, sigma, prefix, paged: PagedKV, workspace,
         info["stage_ms"] = list(inf.stage_ms)
         info["fallback_symbols"] = inf.fallback_symbols
     return st
+
+
+def _tensor(t, name, dtype, shape, device):
+    """A contiguous tensor of this type and shape (None: any extent) on this device."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
+            or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def _queue(device, stream, call, *tensors):
+    """Runs call(stream pointer) with `device` current, on `stream` (the
+    device's current one if None), and keeps the tensors' memory until the
+    work queued there is done."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors of {device}")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.device(device):
+        return call(stream.cuda_stream)
+
+
+class BlockTable:
+    """The pages of a batch of requests, kept on the device: the block table
+    [batch, max_pages], the pages each request holds (held [batch]) and the
+    stack of free pages (free_pages, its height free_count [1]), all int32 and
+    the caller's; a call updates them in place, or writes held_out and
+    free_count_out where they are given.  The step's rows come back in
+    row_starts [batch + 1] (int32), slots [max_rows] (int64) and positions
+    [max_rows] (int32; either may be None).  Holds the call's workspace, so
+    that repeated calls allocate nothing."""
+
+    def __init__(self, block_table, held, free_pages, free_count, page_tokens: int, num_pages: int, row_starts,
+                 slots=None, positions=None, held_out=None, free_count_out=None):
+        _need(block_table, "block_table")
+        dev = block_table.device
+        if block_table.dim() != 2 or block_table.dtype != torch.int32:
+            raise ValueError("block_table must be int32 [batch, max_pages]")
+        batch = block_table.shape[0]
+        _tensor(free_pages, "free_pages", torch.int32, (None,), dev)
+        for t, name in ((free_count, "free_count"), (free_count_out, "free_count_out")):
+            if t is not None:
+                _tensor(t, name, torch.int32, (1,), dev)
+        for t, name in ((held, "held"), (held_out, "held_out")):
+            if t is not None:
+                _tensor(t, name, torch.int32, (batch,), dev)
+        _tensor(row_starts, "row_starts", torch.int32, (batch + 1,), dev)
+        given = [t for t in (slots, positions) if t is not None]
+        max_rows = given[0].shape[0] if given else 0x7FFFFFFF
+        if slots is not None:
+            _tensor(slots, "slots", torch.int64, (max_rows,), dev)
+        if positions is not None:
+            _tensor(positions, "positions", torch.int32, (max_rows,), dev)
+        self.device, self.batch = dev, batch
+        self.block_table, self.free_pages, self.row_starts = block_table, free_pages, row_starts
+        self.slots, self.positions = slots, positions
+        self.held, self.free_count = held, free_count
+        self.held_out = held if held_out is None else held_out
+        self.free_count_out = free_count if free_count_out is None else free_count_out
+        self.workspace = torch.zeros(256 + 12 * (batch + 64), dtype=torch.uint8, device=dev)
+        self.desc = kvc_block_table(
+            batch, block_table.shape[1], num_pages, free_pages.numel(), max_rows, page_tokens, 0, None, None,
+            _ptr(held), _ptr(self.held_out), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
+            _ptr(self.free_count_out), _ptr(row_starts), _ptr(slots), _ptr(positions))
+        self._ref = ctypes.byref(self.desc)
+
+    def __call__(self, cached_lens=None, new_lens=None, trim: bool = False, stream=None):
+        """Queue the step of requests with cached_lens tokens that get
+        new_lens more (int32 [batch]; None: no request has any); result()
+        gives its outcome."""
+        for t, name in ((cached_lens, "cached_lens"), (new_lens, "new_lens")):
+            if t is not None:
+                _tensor(t, name, torch.int32, (self.batch,), self.device)
+        d = self.desc
+        d.trim = 1 if trim else 0
+        d.d_cached_lens, d.d_new_lens = _ptr(cached_lens), _ptr(new_lens)
+        ws = self.workspace
+        st = _queue(self.device, stream,
+                    lambda s: _lib_block_table(self._ref, ws.data_ptr(), ws.numel(), s, None),
+                    cached_lens, new_lens, ws, self.block_table, self.held, self.held_out, self.free_pages,
+                    self.free_count, self.free_count_out, self.row_starts, self.slots, self.positions)
+        _check(st, "kvc_build_block_table")
+
+    def result(self, stream=None) -> int:
+        """The number of rows of the last step; raises KvcError if it failed."""
+        n = _I64(0)
+        st = _queue(self.device, stream,
+                    lambda s: _lib_block_table_result(self.workspace.data_ptr(), s, ctypes.byref(n)))
+        _check(st, "kvc_build_block_table")
+        return n.value
+
+
+def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                     k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Queue the append of the rows k and v [rows, heads, channels] (views of
+    wider rows allowed) to the slots [rows] (int64; -1: none) of one layer's
+    pages; bf16 rows of an e4m3 cache are rounded from x / scale."""
+    dev = paged.block_table.device
+    rows = slots.shape[0]
+    _tensor(slots, "slots", torch.int64, (None,), dev)
+    heads, ch = paged.desc.heads, paged.channels
+    for t, name in ((k, "k"), (v, "v")):
+        if t.device != dev or t.shape != (rows, heads, ch) or (rows and t.stride()[1:] != (ch, 1)) or t.dtype != k.dtype:
+            raise ValueError(f"{name} must be [{rows}, {heads}, {ch}] on {dev}, a row's values contiguous")
+    st = _queue(dev, stream,
+                lambda s: _lib_append(paged.ref, layer, paged.kv_dtype, ch, k.data_ptr(), v.data_ptr(), _kv_dtype(k),
+                                      rows, k.stride(0), v.stride(0), slots.data_ptr(), k_scale, v_scale, s),
+                k, v, slots, paged.ptrs, *(paged.pools if stream is not None else ()))
+    _check(st, "kvc_paged_append")
+
+
+class PagedAttention:
+    """Attention of drafted tokens over a paged cache: holds the workspace of
+    one shape (q_heads query heads, up to max_rows rows a call) so that
+    repeated calls allocate nothing.  rows_per_sequence and max_tokens (the
+    usual rows of a sequence and the longest sequence) shape the launch only;
+    0: max_rows / batch and what the table can hold.  softmax_scale defaults
+    to channels ** -0.5.  Calls that may run at the same time need an object
+    each."""
+
+    def __init__(self, paged: PagedKV, q_heads: int, max_rows: int, rows_per_sequence: int = 0, max_tokens: int = 0,
+                 softmax_scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0):
+        self.paged, self.q_heads, self.max_rows = paged, q_heads, max_rows
+        self.device = paged.block_table.device
+        self.batch, ch = paged.desc.batch, paged.channels
+        scale = ch ** -0.5 if softmax_scale is None else softmax_scale
+        # fixed here: with one launch shape a call of fewer rows needs no larger workspace
+        rows_per_sequence = rows_per_sequence or -(-max_rows // self.batch)
+        self.desc = kvc_attention(None, q_heads * ch, ch, None, q_heads * ch, None, None, None, None, 0, max_rows,
+                                  rows_per_sequence, max_tokens, q_heads, ch, paged.kv_dtype, scale, k_scale, v_scale)
+        self._ref = ctypes.byref(self.desc)
+        n = _U64(0)
+        _check(_lib_attention_sizes(paged.ref, self._ref, ctypes.byref(n)), "kvc_paged_attention_sizes")
+        self.workspace = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, layer: int, q: torch.Tensor, row_starts: torch.Tensor, context_lens: torch.Tensor | None = None,
+                 tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, stream=None):
+        """Queue the attention of q [rows, q_heads, channels] (bf16, views
+        allowed) over one layer's pages; row_starts [batch + 1] and
+        context_lens [batch] int32, tree_mask [rows, words] int64 (bit j of a
+        row: it sees drafted token j) or None (it sees those before it and
+        itself).  Returns (out, lse); result() gives the outcome."""
+        d, dev, ch = self.desc, self.device, self.paged.channels
+        rows = q.shape[0]
+        if q.dtype != torch.bfloat16 or q.device != dev or q.shape[1:] != (self.q_heads, ch) or \
+                (rows and q.stride(2) != 1) or rows > self.max_rows:
+            raise ValueError(f"q must be bf16 [up to {self.max_rows}, {self.q_heads}, {ch}] on {dev}, channels contiguous")
+        _tensor(row_starts, "row_starts", torch.int32, (self.batch + 1,), dev)
+        if context_lens is not None:
+            _tensor(context_lens, "context_lens", torch.int32, (self.batch,), dev)
+        if tree_mask is not None:
+            _tensor(tree_mask, "tree_mask", torch.int64, (rows, None), dev)
+        if out is None or lse is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty((rows, self.q_heads, ch), dtype=q.dtype, device=dev) if out is None else out
+                lse = torch.empty((rows, self.q_heads), dtype=torch.float32, device=dev) if lse is None else lse
+        if out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or \
+                (rows and out.stride()[1:] != (ch, 1)):
+            raise ValueError(f"out must be bf16 {list(q.shape)} on {dev}, a row's values contiguous")
+        _tensor(lse, "lse", torch.float32, (rows, self.q_heads), dev)
+        d.d_q, d.q_row_stride, d.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+        d.d_out, d.out_row_stride, d.d_lse = out.data_ptr(), out.stride(0), lse.data_ptr()
+        d.d_row_starts, d.d_context_lens = row_starts.data_ptr(), _ptr(context_lens)
+        d.d_tree_mask, d.mask_words = _ptr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1]
+        d.rows = rows
+        ws, paged = self.workspace, self.paged
+        st = _queue(dev, stream,
+                    lambda s: _lib_attention(paged.ref, layer, self._ref, ws.data_ptr(), ws.numel(), s),
+                    q, out, lse, row_starts, context_lens, tree_mask, ws, paged.ptrs, paged.block_table,
+                    *(paged.pools if stream is not None else ()))
+        _check(st, "kvc_paged_attention")
+        return out, lse
+
+    def result(self, stream=None) -> None:
+        """Waits for the last call; raises KvcError if it met lengths or page
+        numbers that do not fit."""
+        st = _queue(self.device, stream, lambda s: _lib_attention_result(self.workspace.data_ptr(), s))
+        _check(st, "kvc_paged_attention")
+
+
+def kvc_paged_attention(paged: PagedKV, layer: int, q: torch.Tensor, row_starts: torch.Tensor,
+                        context_lens: torch.Tensor | None = None, tree_mask: torch.Tensor | None = None,
+                        softmax_scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """One call of PagedAttention, waited for: (out [rows, q_heads, channels]
+    bf16, lse [rows, q_heads] float32)."""
+    with torch.cuda.stream(stream):
+        att = PagedAttention(paged, q.shape[1], q.shape[0], softmax_scale=softmax_scale, k_scale=k_scale,
+                             v_scale=v_scale)
+    got = att(layer, q, row_starts, context_lens, tree_mask, stream=stream)
+    att.result(stream)
+    return got
 
 
 def calibrate_workspace_bytes(planes: int, channels: int) -> int:

@@ -364,6 +364,166 @@ int kvc_decode_paged(const void* h_header, const void* d_in, uint64_t in_bytes,
                      void* stream, kvc_decode_info* h_info);
 
 /*
+ * The paged cache around a decode: the calls below build the block table
+ * that kvc_decode_paged and the attention read, append a step's new K/V rows
+ * to its pages, and attend to them.  None of them synchronises unless its
+ * declaration says so, and each launches kernels only (no memset, no copy),
+ * so that all of them may be captured in a HIP graph and replayed; calls
+ * that may run at the same time need workspaces of their own.
+ */
+
+/*
+ * Block tables and slot maps from request lengths.  Request b holds
+ * d_held_in[b] pages (the first entries of its row of d_block_table) and
+ * d_cached_lens[b] tokens, and gets d_new_lens[b] more this step; free pages
+ * are a stack, d_free_pages[0 .. *d_free_in), the last entry on top.  With
+ * P = page_tokens and need_b = ceil((cached_b + new_b) / P):
+ *   - request b takes max(0, need_b - held_b) pages from the top of the stack,
+ *     requests in order, each request's pages in order; they are appended to
+ *     its row of the table;
+ *   - with trim = 1 a request that holds more than need_b pages first gives
+ *     the surplus back (a finished request, cached = new = 0, gives all), in
+ *     such an order that trimming what a call just took restores the stack;
+ *     without it (0) surplus pages stay with the request.  A page that stands
+ *     in several requests' rows must not be trimmed;
+ *   - d_held_out[b] = need_b with trim, else max(held_b, need_b), *d_free_out
+ *     the stack's new height.  d_held_out / d_free_out may be d_held_in /
+ *     d_free_in (the state is updated in place) or other arrays (the old state
+ *     stays readable; the pages given back are written above the old top);
+ *   - the step's new tokens are rows, request after request: d_row_starts[b]
+ *     is the first of request b, d_row_starts[batch] their number.  Row r, the
+ *     i-th new token of request b, has d_positions[r] = cached_b + i and
+ *     d_slots[r] = page x P + position % P, the page being the table's for
+ *     position / P.  Rows behind the last, up to max_rows, get -1 in both.
+ * Entries of the table behind a request's pages are left as they were.
+ * On an error (kvc_block_table_result): KVC_ERR_INVALID for a negative length,
+ * a held count outside [0, max_pages] or a *d_free_in outside [0,
+ * free_capacity]; KVC_ERR_CAPACITY where a request needs more than max_pages
+ * pages or 2^31 tokens, the step more pages than are free, more than max_rows
+ * rows, or a trim more than free_capacity entries.  The table, the stack, the
+ * held counts and the height are then what they were, every row start is 0
+ * and every slot and position -1, so that what is queued behind it appends
+ * and attends to nothing.  A page number outside [0, num_pages), in the stack
+ * or the table, is KVC_ERR_INVALID too: rows on such a page get slot -1, the
+ * rest is written.
+ * h_rows == NULL makes the call asynchronous; otherwise it synchronises
+ * `stream` once, sets *h_rows to the number of rows and returns the outcome.
+ * Workspace: KVC_BLOCK_TABLE_WORKSPACE_BYTES(batch), 256-byte aligned.
+ */
+#define KVC_BLOCK_TABLE_WORKSPACE_BYTES(batch) (256u + 12u * ((uint64_t)(batch) + 64u))
+typedef struct kvc_block_table {
+    int64_t batch;                  /* requests                                       */
+    int64_t max_pages;              /* row stride of the table; batch x max_pages < 2^31 */
+    int64_t num_pages;              /* pages in every pool, < 2^31                    */
+    int64_t free_capacity;          /* entries of d_free_pages, < 2^31                */
+    int64_t max_rows;               /* entries of d_slots and d_positions, < 2^31     */
+    uint32_t page_tokens;           /* tokens per page                                */
+    uint32_t trim;                  /* 0 or 1                                         */
+    const int32_t* d_cached_lens;   /* [batch]; NULL: no request has any              */
+    const int32_t* d_new_lens;      /* [batch]; NULL: no request gets any             */
+    const int32_t* d_held_in;       /* [batch]                                        */
+    int32_t* d_held_out;            /* [batch]                                        */
+    int32_t* d_block_table;         /* [batch][max_pages]                             */
+    int32_t* d_free_pages;          /* [free_capacity]                                */
+    const int32_t* d_free_in;       /* [1]                                            */
+    int32_t* d_free_out;            /* [1]                                            */
+    int32_t* d_row_starts;          /* [batch + 1]                                    */
+    int64_t* d_slots;               /* [max_rows] (NULL allowed)                      */
+    int32_t* d_positions;           /* [max_rows] (NULL allowed)                      */
+} kvc_block_table;
+int kvc_build_block_table(const kvc_block_table* p, void* d_workspace, uint64_t workspace_bytes,
+                          void* stream, int64_t* h_rows);
+
+/*
+ * Outcome of the last kvc_build_block_table queued with this workspace:
+ * synchronises `stream` once, returns its status and sets *h_rows (may be
+ * NULL) to the number of rows.
+ */
+int kvc_block_table_result(const void* d_workspace, void* stream, int64_t* h_rows);
+
+/*
+ * New K/V rows into the pages of one layer: row r of d_k ([rows] rows of
+ * heads x channels values of src_dtype, row_stride values apart) goes to slot
+ * d_slots[r] of pool 2 x layer, row r of d_v to the same slot of pool 2 x
+ * layer + 1, a slot being page x page_tokens + row as kvc_build_block_table
+ * gives it.  Rows whose slot is negative or past the pool are skipped; two
+ * rows of one slot leave a mix of both.  kv_dtype is the pools' type:
+ * values of the same type are copied bit for bit; bf16 into e4m3 is
+ * x / k_scale (x / v_scale) rounded to nearest even, what lies beyond +-448
+ * saturated, NaN kept.  Scales are finite and positive, and 1 when the types
+ * are the same.  h_paged as for kvc_decode_paged (its table is not read and
+ * may be NULL).  d_k and d_v 16-byte aligned, row strides (in values, at
+ * least heads x channels when rows > 1) such that every row is.  Does not
+ * synchronise; KVC_ERR_INVALID for bad arguments, nothing launched.
+ */
+int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtype, int64_t channels,
+                     const void* d_k, const void* d_v, int32_t src_dtype, int64_t rows,
+                     int64_t k_row_stride, int64_t v_row_stride, const int64_t* d_slots,
+                     float k_scale, float v_scale, void* stream);
+
+/*
+ * Attention of drafted tokens over a paged cache.  Sequence b of h_paged's
+ * batch has d_context_lens[b] tokens in its pages that every row of it sees,
+ * and behind them its n_b = d_row_starts[b + 1] - d_row_starts[b] drafted
+ * tokens (already appended, at positions context_b + 0 .. n_b - 1); row
+ * d_row_starts[b] + i of d_q is drafted token i.  It sees drafted token j
+ * where bit j % 64 of word j / 64 of its row of d_tree_mask ([rows]
+ * [mask_words]) is set, j < n_b (bits behind n_b are ignored); without a
+ * mask (NULL) it sees j <= i: a chain, a piece of a prompt or, n_b = 1, the
+ * next token.  With query head a reading KV head a / (q_heads / heads):
+ *     s_t = softmax_scale x k_scale x <q, K_t>,
+ *     o = v_scale x sum_t e^(s_t) V_t / sum_t e^(s_t)  over the tokens seen,
+ *     lse = log sum_t e^(s_t);
+ * a row that sees nothing has o = 0 and lse = -infinity.  What K or V hold
+ * (NaN, infinity) at tokens that a row does not see has no part in it.  Sums,
+ * maxima and the output's accumulation are float32; the weights e^(s - max)
+ * are rounded to bf16 for the matrix instructions (see the kernel), the
+ * output to bf16.  Rows behind d_row_starts[batch] are left as they were.
+ * q and out bf16, the cache bf16 or e4m3; channels 64, 128, 192 or 256;
+ * q_heads a multiple of heads, at most 1024 per KV head.  num_pages x
+ * page_tokens < 2^31.
+ * rows_per_sequence and max_tokens shape the launch only; results do not
+ * depend on them: the usual n_b (0: rows / batch) and the longest context +
+ * n_b (0: max_pages x page_tokens).
+ * Does not synchronise.  kvc_paged_attention_result gives KVC_ERR_INVALID
+ * where row starts fall or pass `rows`, a context is negative, a sequence
+ * passes max_pages x page_tokens tokens (that sequence's rows are not
+ * written), or a page number read lies outside [0, num_pages) (page 0 is
+ * read in its place: its rows are undefined).
+ * Workspace: kvc_paged_attention_sizes, 256-byte aligned.
+ */
+typedef struct kvc_attention {
+    const void* d_q;                /* [rows][q_heads][channels] bf16                 */
+    int64_t q_row_stride;           /* in values, multiples of 8                      */
+    int64_t q_head_stride;
+    void* d_out;                    /* [rows][q_heads][channels] bf16                 */
+    int64_t out_row_stride;         /* in values, multiples of 8; heads are channels apart */
+    float* d_lse;                   /* [rows][q_heads] or NULL                        */
+    const int32_t* d_row_starts;    /* [batch + 1]                                    */
+    const int32_t* d_context_lens;  /* [batch]; NULL: none has any                    */
+    const uint64_t* d_tree_mask;    /* [rows][mask_words] or NULL                     */
+    int64_t mask_words;             /* 0 without a mask                               */
+    int64_t rows;                   /* rows of q and out, < 2^24                      */
+    int64_t rows_per_sequence;
+    int64_t max_tokens;
+    int64_t q_heads;
+    int64_t channels;
+    int32_t kv_dtype;               /* KVC_BF16 or KVC_E4M3                           */
+    float softmax_scale;
+    float k_scale, v_scale;         /* finite, positive                               */
+} kvc_attention;
+int kvc_paged_attention_sizes(const kvc_paged_kv* h_paged, const kvc_attention* p,
+                              uint64_t* h_workspace_bytes);
+int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_attention* p,
+                        void* d_workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * Outcome of the last kvc_paged_attention queued with this workspace:
+ * synchronises `stream` and returns its status.
+ */
+int kvc_paged_attention_result(const void* d_workspace, void* stream);
+
+/*
  * Sigma calibration ([wiki] "predictor choice": per-(kv, head, channel)
  * variance calibrated on data, then frozen; [blog] "deployment parameters":
  * 128 sequences of 1024 tokens).  d_kv and d_mu are [reps][planes][tokens]
