@@ -23,6 +23,8 @@
 //     lane; row i of the c-th product is then channel i C + c.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kvc_paged.hpp"
 
 namespace kvc {
@@ -31,6 +33,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
@@ -109,7 +112,8 @@ __device__ Share share_of(const AttendArgs& a, uint32_t id, uint32_t tile_rows, 
         const uint32_t half = a.target / 2;
         const uint32_t parts = items < half ? a.target - static_cast<uint32_t>(items) : half;
         const float want = float(units) / float(parts) + 1.0f;
-        per = want < float(kWaves) ? kWaves : want > 2e9f ? 2000000000u : static_cast<uint32_t>(want);
+        // whole rounds of the four waves
+        per = want > 2e9f ? 2000000000u : (static_cast<uint32_t>(want) + kWaves - 1) / kWaves * kWaves;
     }
     Share r{};
     uint64_t base = 0;
@@ -193,38 +197,51 @@ __device__ uint32_t widen(uint32_t four) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.0f, HIGH));
 }
 
-// WORDS 32-bit words from p (aligned to what WORDS allows).
+// The pools' addresses are read from memory: that they are global ones has
+// to be said.
+#define GLOBAL __attribute__((address_space(1)))
+typedef const GLOBAL uint8_t* GlobalBytes;
+
+// WORDS 32-bit words, in the vectors that they are loaded as: kept whole,
+// they stay in the registers that the loads write.
 template <int WORDS>
-__device__ void load_words(uint32_t (&x)[WORDS], const uint8_t* p) {
-    if constexpr (WORDS % 4 == 0) {
+struct Words {
+    static constexpr int W = WORDS % 4 == 0 ? 4 : WORDS % 2 == 0 ? 2 : 1;
+    typedef uint32_t Vec __attribute__((ext_vector_type(W)));
+    Vec v[WORDS / W];
+
+    __device__ uint32_t operator[](int i) const { return v[i / W][i % W]; }
+    __device__ void set(int i, uint32_t x) { v[i / W][i % W] = x; }
+    __device__ void load(GlobalBytes p) {
 #pragma unroll
-        for (int i = 0; i < WORDS; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
-            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-        }
-    } else if constexpr (WORDS % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
-            x[i] = v.x, x[i + 1] = v.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) x[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+        for (int i = 0; i < WORDS / W; ++i) v[i] = *reinterpret_cast<const GLOBAL Vec*>(p + 4 * W * i);
     }
-}
+};
 
 __device__ uint32_t two_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
-// Whether a 16-bit half is an infinity or a NaN, and its class as a bf16
-// power of two: +infinity 1, -infinity 2^8, NaN 2^16 (sums of up to 32 of
-// each are told apart in a float32 sum).
+// Infinities and NaN among a word's values (two bf16; four e4m3, which has
+// no infinity): the top bit of each value's place is set where it is one.
 __device__ bool wild_half(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
-__device__ uint32_t class_half(uint32_t h) {
-    if (!wild_half(h)) return 0u;
-    return (h & 0x7Fu) ? 0x4780u : (h & 0x8000u) ? 0x4380u : 0x3F80u;
+
+template <bool FP8>
+__device__ uint32_t wild_bits(uint32_t w) {
+    return FP8 ? ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+template <bool FP8>
+__device__ uint32_t without_wild(uint32_t w) {
+    return w & ~(FP8 ? (wild_bits<true>(w) >> 7) * 0xFFu : (wild_bits<false>(w) >> 15) * 0xFFFFu);
+}
+
+// Value c of words (w is its word) if it is an infinity or a NaN, else zero.
+template <bool FP8>
+__device__ float wild_part(uint32_t w, int c) {
+    if constexpr (FP8) return ((w >> (8 * (c & 3))) & 0x7Fu) == 0x7Fu ? __builtin_nanf("") : 0.0f;
+    const uint32_t h = (c & 1) ? w >> 16 : w;
+    return wild_half(h) ? __uint_as_float(h << 16) : 0.0f;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -235,8 +252,32 @@ struct Lds {
     float m[kWaves][16 * RT], l[kWaves][16 * RT];
 };
 
-template <int D, bool FP8, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_attend(AttendArgs a) {
+// Words read through the scalar cache: they are not written while the kernel
+// runs, and every lane wants the same ones.
+__device__ int32_t uniform_word(const int32_t* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
+}
+
+// The largest of the four lanes n, n + 16, n + 32, n + 48.
+__device__ float top_of_column(float x) {
+    u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Waves that a SIMD can hold at once, from the registers that a wave needs:
+// queries, a tile of K and of V, the sums, scores and weights, and about 50
+// for the rest, of 512.
+constexpr int waves_of(int d, bool fp8, int rt) {
+    const int need = d * rt / 8 + 2 * (d * (fp8 ? 1 : 2) / 8) + d * rt / 4 + 12 * rt + 44;
+    return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+}
+
+// PAGE16: pages are a multiple of 16 tokens, so that a half of a tile lies in
+// one page and its rows are a constant stride apart.
+template <int D, bool FP8, int RT, bool PAGE16>
+__global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8, RT)) void k_attend(AttendArgs a) {
     constexpr int C = D / 16;                   // channels of V a lane holds
     constexpr int ES = FP8 ? 1 : 2;
     constexpr int VW = C * ES / 4;              // words of them
@@ -244,7 +285,8 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
     constexpr int KK = D / 32;                  // products over the channels
     __shared__ Lds<D, FP8, RT> lds;
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, q4 = lane >> 4;
     const Share sh = share_of(a, blockIdx.x, 16 * RT, gridDim.x);
     uint32_t bad_page = 0;
@@ -260,12 +302,16 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
         const int ta = static_cast<int>(uint64_t(tiles) * sh.split / sh.splits);
         const int tb = static_cast<int>(uint64_t(tiles) * (sh.split + 1) / sh.splits);
 
+        const uint32_t num_pages = static_cast<uint32_t>(a.num_pages);     // x page_tokens < 2^31
         const uint32_t row_bytes = a.heads * D * ES;
-        const uint8_t* const kp = static_cast<const uint8_t*>(a.pools[0]) + sh.head * (D * ES);
-        const uint8_t* const vp = static_cast<const uint8_t*>(a.pools[1]) + sh.head * (D * ES);
+        const GlobalBytes kp = reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[0])) + sh.head * (D * ES);
+        const GlobalBytes vp = reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[1])) + sh.head * (D * ES);
         const int32_t* const table = a.block_table + int64_t(sh.b) * a.max_pages;
 
-        // the query rows, as the second operand of K Q^T
+        // The query rows, as the second operand of K Q^T.  The scale is made positive by their sign, so that the
+        // largest scaled score is the scaled largest score; a scale of zero becomes the smallest one.
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
         bf16x8 qf[RT][KK];
         int node[RT];
 #pragma unroll
@@ -280,12 +326,12 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
             for (int kk = 0; kk < KK; ++kk) {
                 const int ch = FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4;
                 const uint4 x = real ? *reinterpret_cast<const uint4*>(q + ch) : uint4{0, 0, 0, 0};
-                qf[rt][kk] = frag_of(x.x, x.y, x.z, x.w);
+                qf[rt][kk] = frag_of(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
             }
         }
 
         f32x4 o[RT][C];
-        float mx[RT], l[RT];
+        float mx[RT], l[RT];                    // mx: of the scores before their scale
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             mx[rt] = kNegInf;
@@ -294,36 +340,86 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
             for (int c = 0; c < C; ++c) o[rt][c] = f32x4{0, 0, 0, 0};
         }
 
-        // slot of token t (of the last one, for those behind it): page x page_tokens + row
-        auto slot_of = [&](int t) -> uint32_t {
-            const uint32_t at = static_cast<uint32_t>(t < length ? t : length - 1);
-            const uint32_t j = at / a.page_tokens;
-            int32_t page = table[j];
-            if (page < 0 || page >= a.num_pages) {
+        // Where a tile's tokens lie: with PAGE16 the page numbers of its halves, otherwise this lane's slot (page x
+        // page_tokens + row of token lane % 32).  Tokens behind the last one take its place.
+        struct Where {
+            int32_t page[2];
+            uint32_t slot;
+        };
+        auto find = [&](int t) -> Where {
+            Where w{};
+            if constexpr (PAGE16) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int at = t * kTile + hf * 16;
+                    const uint32_t tok = static_cast<uint32_t>(at < length ? at : length - 1);
+                    w.page[hf] = uniform_word(table + ((uint64_t(tok) * a.page_mul) >> a.page_shift));
+                }
+            } else {
+                const int at = t * kTile + (lane & 31);
+                const uint32_t tok = static_cast<uint32_t>(at < length ? at : length - 1);
+                const uint32_t j = static_cast<uint32_t>((uint64_t(tok) * a.page_mul) >> a.page_shift);
+                uint32_t page = static_cast<uint32_t>(table[j]);
+                if (page >= num_pages) {
+                    bad_page = kPagedInvalid;
+                    page = 0;
+                }
+                w.slot = page * a.page_tokens + (tok - j * a.page_tokens);
+            }
+            return w;
+        };
+        // byte offset of a half's first row in its pool
+        auto half_at = [&](const Where& w, int t, int hf) -> uint64_t {
+            const int at = t * kTile + hf * 16;
+            const uint32_t tok = static_cast<uint32_t>(at < length ? at : (length - 1) & ~15);
+            const uint32_t j = static_cast<uint32_t>((uint64_t(tok) * a.page_mul) >> a.page_shift);
+            uint32_t page = static_cast<uint32_t>(w.page[hf]);
+            if (page >= num_pages) {
                 bad_page = kPagedInvalid;
                 page = 0;
             }
-            return static_cast<uint32_t>(page) * a.page_tokens + (at - j * a.page_tokens);
+            return uint64_t(page * a.page_tokens + (tok - j * a.page_tokens)) * row_bytes;
         };
 
-        int t = ta + wave;
-        uint32_t slot = t < tb ? slot_of(t * kTile + (lane & 31)) : 0u;
-        for (; t < tb; t += kWaves) {
-            const int t0 = t * kTile;
-            // K: token n of each half, V: the eight tokens of this lane's scores
-            uint32_t kw[2][KG][4], vw[8][VW];
+        // K: token n of each half; V: the eight tokens of this lane's scores
+        Words<4> kw[2][KG];
+        Words<VW> vw[8];
+        auto load_k = [&](const Where& w, int t) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const uint8_t* const p = kp + uint64_t(__shfl(slot, hf * 16 + n)) * row_bytes + 16 * q4;
+                const GlobalBytes p = PAGE16
+                    ? kp + half_at(w, t, hf) + (uint32_t(n) * row_bytes + 16u * q4)
+                    : kp + uint64_t(__shfl(w.slot, hf * 16 + n)) * row_bytes + 16 * q4;
 #pragma unroll
-                for (int kg = 0; kg < KG; ++kg) load_words(kw[hf][kg], p + 64 * kg);
+                for (int kg = 0; kg < KG; ++kg) kw[hf][kg].load(p + 64 * kg);
             }
+        };
+        auto load_v = [&](const Where& w, int t) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int x = (j < 4 ? 0 : 12) + q4 * 4 + j;
-                load_words(vw[j], vp + uint64_t(__shfl(slot, x)) * row_bytes + n * (C * ES));
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint64_t at = PAGE16 ? half_at(w, t, hf) : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const GlobalBytes p = PAGE16
+                        ? vp + at + (uint32_t(q4 * 4 + j) * row_bytes + uint32_t(n) * (C * ES))
+                        : vp + uint64_t(__shfl(w.slot, hf * 16 + q4 * 4 + j)) * row_bytes + n * (C * ES);
+                    vw[hf * 4 + j].load(p);
+                }
             }
-            slot = slot_of((t + kWaves) * kTile + (lane & 31));
+        };
+
+        // A wave takes every fourth tile.  Its K registers are free once the scores are formed and its V registers
+        // once they are summed, so the next tile's K is under way during the weights and the sum, and its V during
+        // the next scores and weights.  That is the loop over tiles that every row sees in full; the others (and the
+        // last one) go through a second copy of the body, which knows of masks and prefetches nothing, so that the
+        // first has no loads under a condition, which would be waited for with the count of the other path.
+        const int full = ctx + (a.mask ? 0 : row0 / static_cast<int>(a.ratio) + 1);
+        bool any_wild = false;
+        auto one_tile = [&](int t, auto inner) {
+            const int t0 = t * kTile;
+            const int next = t + kWaves;
+            Where w{};
+            if constexpr (inner) w = find(next);
 
             // scores
             f32x4 s[RT][2];
@@ -338,97 +434,89 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
                         const uint32_t lo = kw[hf][kk / 2][2 * (kk & 1)], hi = kw[hf][kk / 2][2 * (kk & 1) + 1];
                         kf = frag_of(widen<false>(lo), widen<true>(lo), widen<false>(hi), widen<true>(hi));
                     } else {
-                        kf = frag_of(kw[hf][kk][0], kw[hf][kk][1], kw[hf][kk][2], kw[hf][kk][3]);
+                        kf = __builtin_bit_cast(bf16x8, kw[hf][kk].v[0]);
                     }
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
                         s[rt][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][kk], s[rt][hf], 0, 0, 0);
                 }
             }
+            // (held in place: started any earlier, the loads need registers of their own)
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (inner) load_k(w, next);
+            __builtin_amdgcn_sched_barrier(0);
 
-            // Tiles with drafted tokens (or none behind the last): what a row sees is a window of 32 bits.  V values
-            // of unseen tokens meet weights of zero, which an infinity or a NaN would turn into NaN: tokens behind
-            // the last are cleared, and where a drafted one holds any such value the tile takes a way of its own.
-            const bool edge = t0 + kTile > ctx;
-            uint32_t win[RT];
-            bool wild = false;
-            if (edge) {
+            // What a row sees of a tile is a window of 32 bits.  V values of unseen tokens meet weights of zero, which
+            // an infinity or a NaN would turn into NaN: tokens behind the last are cleared, and so are such values of
+            // drafted ones; they are added at the end to the rows that see them.
+            if (!inner && t0 + kTile > full) {
+                uint32_t wild = 0;
                 const int j0 = t0 - ctx;                              // > -32
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    uint32_t w;
+                    uint32_t w32;
                     if (a.mask) {
                         const uint64_t* const bits =
                             a.mask + (int64_t(sh.seq.start) + node[rt]) * a.mask_words;
                         if (j0 < 0) {
-                            w = (static_cast<uint32_t>(bits[0]) << -j0) | ((1u << -j0) - 1u);
+                            w32 = (static_cast<uint32_t>(bits[0]) << -j0) | ((1u << -j0) - 1u);
                         } else {
                             const uint32_t at = static_cast<uint32_t>(j0) >> 6, by = j0 & 63;
                             uint64_t x = at < a.mask_words ? bits[at] >> by : 0u;
                             if (by > 32 && at + 1 < a.mask_words) x |= bits[at + 1] << (64 - by);
-                            w = static_cast<uint32_t>(x);
+                            w32 = static_cast<uint32_t>(x);
                         }
                         const int there = sh.seq.rows - j0;           // >= 1
-                        if (there < 32) w &= (1u << there) - 1u;
+                        if (there < 32) w32 &= (1u << there) - 1u;
                     } else {
                         const int see = node[rt] - j0 + 1;
-                        w = see >= 32 ? 0xFFFFFFFFu : see <= 0 ? 0u : (1u << see) - 1u;
+                        w32 = see >= 32 ? 0xFFFFFFFFu : see <= 0 ? 0u : (1u << see) - 1u;
                     }
-                    win[rt] = w;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (!((w32 >> ((j < 4 ? 0 : 12) + q4 * 4 + j)) & 1u)) s[rt][j >> 2][j & 3] = kNegInf;
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int tok = t0 + (j < 4 ? 0 : 12) + q4 * 4 + j;
+                    const uint32_t there = tok < length ? ~0u : 0u, drafted = tok >= ctx ? ~0u : 0u;
 #pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        if (tok >= length) vw[j][w] = 0u;
-                        if (tok >= ctx) {
-                            if constexpr (FP8) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) wild = wild || ((vw[j][w] >> (8 * i)) & 0x7Fu) == 0x7Fu;
-                            } else {
-                                wild = wild || wild_half(vw[j][w]) || wild_half(vw[j][w] >> 16);
-                            }
-                        }
+                    for (int x = 0; x < VW; ++x) {
+                        vw[j].set(x, vw[j][x] & there);
+                        wild |= wild_bits<FP8>(vw[j][x]) & drafted;
                     }
                 }
-                wild = __any(wild);
+                if (__any(wild != 0)) {
+                    any_wild = true;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) vw[j].set(x, without_wild<FP8>(vw[j][x]));
+                }
             }
 
-            // weights
+            // weights 2^(scale (s - max))
             bf16x8 pf[RT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = s[rt][j >> 2][j & 3] * a.scale_log2;
-                if (edge) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!((win[rt] >> ((j < 4 ? 0 : 12) + q4 * 4 + j)) & 1u)) x[j] = kNegInf;
-                }
-                float top = x[0];
-#pragma unroll
-                for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                top = fmaxf(top, mx[rt]);
+                const f32x4 x = s[rt][0], y = s[rt][1];
+                float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+                top = fmaxf(top_of_column(top), mx[rt]);
                 const float zero = top == kNegInf ? 0.0f : top;
                 if (__any(top > mx[rt])) {
-                    const float f = __builtin_amdgcn_exp2f(mx[rt] - zero);
+                    const float f = __builtin_amdgcn_exp2f((mx[rt] - zero) * scale);
                     l[rt] *= f;
 #pragma unroll
                     for (int c = 0; c < C; ++c) o[rt][c] *= f;
                     mx[rt] = top;
                 }
-                float sum = 0.0f;
+                const float shift = -zero * scale;
+                float e[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] = __builtin_amdgcn_exp2f(x[j] - zero);
-                    sum += x[j];
-                }
-                l[rt] += sum;
-                pf[rt] = frag_of(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
+                for (int j = 0; j < 8; ++j)
+                    e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][j >> 2][j & 3], scale, shift));
+                l[rt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                pf[rt] = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
             }
 
             // the weighted sum of V, one product for each of a lane's channels
@@ -437,45 +525,14 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
                 uint32_t f[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const int w = c * ES / 4;
+                    const int x = c * ES / 4;
                     if constexpr (FP8) {
-                        const uint32_t pair = (c & 2) ? __builtin_amdgcn_perm(vw[2 * p + 1][w], vw[2 * p][w], 0x07030602u)
-                                                      : __builtin_amdgcn_perm(vw[2 * p + 1][w], vw[2 * p][w], 0x05010400u);
+                        const uint32_t pair = (c & 2) ? __builtin_amdgcn_perm(vw[2 * p + 1][x], vw[2 * p][x], 0x07030602u)
+                                                      : __builtin_amdgcn_perm(vw[2 * p + 1][x], vw[2 * p][x], 0x05010400u);
                         f[p] = (c & 1) ? widen<true>(pair) : widen<false>(pair);
                     } else {
-                        f[p] = (c & 1) ? __builtin_amdgcn_perm(vw[2 * p + 1][w], vw[2 * p][w], 0x07060302u)
-                                       : __builtin_amdgcn_perm(vw[2 * p + 1][w], vw[2 * p][w], 0x05040100u);
-                    }
-                }
-                if (edge && wild) {
-                    // infinities and NaN go through a product of their own: how many of each class a row sees
-                    uint32_t cls[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        cls[p] = class_half(f[p] & 0xFFFFu) | (class_half(f[p] >> 16) << 16);
-                        if (wild_half(f[p])) f[p] &= 0xFFFF0000u;
-                        if (wild_half(f[p] >> 16)) f[p] &= 0x0000FFFFu;
-                    }
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        uint32_t one[4];
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const int x = (p < 2 ? 0 : 12) + q4 * 4 + 2 * p;
-                            one[p] = (((win[rt] >> x) & 1u) ? 0x3F80u : 0u) |
-                                     (((win[rt] >> (x + 1)) & 1u) ? 0x3F800000u : 0u);
-                        }
-                        const f32x4 seen_of = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            frag_of(cls[0], cls[1], cls[2], cls[3]), frag_of(one[0], one[1], one[2], one[3]),
-                            f32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t k = static_cast<uint32_t>(seen_of[i]);
-                            const bool pos = k & 0xFFu, neg = (k >> 8) & 0xFFu, nan = k >> 16;
-                            if (nan || (pos && neg)) o[rt][c][i] = __builtin_nanf("");
-                            else if (pos) o[rt][c][i] += __builtin_inff();
-                            else if (neg) o[rt][c][i] -= __builtin_inff();
-                        }
+                        f[p] = (c & 1) ? __builtin_amdgcn_perm(vw[2 * p + 1][x], vw[2 * p][x], 0x07060302u)
+                                       : __builtin_amdgcn_perm(vw[2 * p + 1][x], vw[2 * p][x], 0x05040100u);
                     }
                 }
                 const bf16x8 vf = frag_of(f[0], f[1], f[2], f[3]);
@@ -483,7 +540,36 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
                 for (int rt = 0; rt < RT; ++rt)
                     o[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt], o[rt][c], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (inner) load_v(w, next);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int t = ta + wave;
+        if (t < tb) {
+            const Where w = find(t);
+            load_k(w, t);
+            load_v(w, t);
+            const int last = (tb - kWaves < full / kTile ? tb - kWaves : full / kTile) - 1;
+            if (t <= last) {
+                int left = (last - t) / kWaves + 1;
+                do {
+                    one_tile(t, std::true_type{});
+                    t += kWaves;
+                } while (--left);
+            }
+            for (;;) {
+                one_tile(t, std::false_type{});
+                t += kWaves;
+                if (t >= tb) break;
+                const Where v = find(t);
+                load_k(v, t);
+                load_v(v, t);
+            }
         }
+
+        // from here on the maxima are of the scaled scores
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) mx[rt] *= scale;
 
         // the four waves' sums, joined through LDS
 #pragma unroll
@@ -495,7 +581,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
                 lds.l[wave][rt * 16 + n] = l[rt];
             }
         }
-        __syncthreads();
+        any_wild = __syncthreads_or(any_wild);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float top = lds.m[0][rt * 16 + n];
@@ -524,6 +610,26 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 && D <= 128 ? 2 : 1) void k_at
 #pragma unroll
                     for (int w = 1; w < kWaves; ++w)
                         acc[i] += *reinterpret_cast<const f32x4*>(&lds.o[w][lr][part * C + 4 * i]);
+                }
+                if (any_wild) {
+                    // an infinity or a NaN in V is what it makes of every row that sees its token
+                    const int nd = m / static_cast<int>(a.ratio);
+                    const int end = tb * kTile < length ? tb * kTile : length;
+                    for (int tok = ta * kTile > ctx ? ta * kTile : ctx; tok < end; ++tok) {
+                        const uint32_t j = static_cast<uint32_t>(tok - ctx);
+                        const uint64_t* const bits = a.mask + (int64_t(sh.seq.start) + nd) * a.mask_words;
+                        if (a.mask ? j / 64 >= a.mask_words || !((bits[j / 64] >> (j & 63)) & 1u)
+                                   : static_cast<int>(j) > nd)
+                            continue;
+                        const uint32_t at = static_cast<uint32_t>((uint64_t(uint32_t(tok)) * a.page_mul) >> a.page_shift);
+                        uint32_t page = static_cast<uint32_t>(table[at]);
+                        if (page >= num_pages) page = 0;
+                        const uint64_t slot = page * a.page_tokens + (uint32_t(tok) - at * a.page_tokens);
+                        Words<VW> w;
+                        w.load(vp + slot * row_bytes + part * (C * ES));
+#pragma unroll
+                        for (int c = 0; c < C; ++c) acc[c / 4][c & 3] += wild_part<FP8>(w[c * ES / 4], c);
+                    }
                 }
                 if (sh.splits == 1) {
                     const int nd = m / static_cast<int>(a.ratio), g = m - nd * static_cast<int>(a.ratio);
@@ -590,7 +696,6 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, uint32_t tile
             sum = __builtin_fmaf(x.y, f, sum);
         }
         const uint32_t n = span.splits - s0 < 64 ? span.splits - s0 : 64;
-#pragma unroll 4
         for (uint32_t s = 0; s < n; ++s) {
             const float w = __shfl(f, s);
             const float* const p = a.partial + (first + (s0 + s) * step) * D + lane * E;
@@ -613,13 +718,13 @@ int row_tiles_of(int64_t rows, int64_t channels) {
     return rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGE16>
 hipError_t launch(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
     switch (sh.row_tiles) {
-        case 1: k_attend<D, FP8, 1><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
-        case 2: k_attend<D, FP8, 2><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
+        case 1: k_attend<D, FP8, 1, PAGE16><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
+        case 2: k_attend<D, FP8, 2, PAGE16><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
         default:
-            if constexpr (D <= 128) k_attend<D, FP8, 4><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+            if constexpr (D <= 128) k_attend<D, FP8, 4, PAGE16><<<sh.grid, 64 * kWaves, 0, s>>>(a);
             else return hipErrorInvalidValue;
     }
     if (sh.split) {
@@ -633,12 +738,11 @@ hipError_t launch(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
 
 AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t channels, bool fp8, int64_t rows,
                          int64_t rows_per_sequence, int64_t max_tokens) {
-    (void)fp8;
     AttendShape s;
     const int64_t usual = rows_per_sequence > 0 ? rows_per_sequence : (rows + batch - 1) / batch;
     s.row_tiles = row_tiles_of(usual * ratio, channels);
     const int64_t tile_rows = 16 * s.row_tiles;
-    s.target = 256 * (s.row_tiles == 1 && channels <= 128 ? 2 : 1);
+    s.target = 256u * waves_of(static_cast<int>(channels), fp8, s.row_tiles);
     s.split = (max_tokens + kTile - 1) / kTile > kWaves;
     // every sequence's rows fill whole tiles but the last one
     const uint64_t items = uint64_t(heads) * (uint64_t(rows) * ratio / tile_rows + (rows < batch ? rows : batch));
@@ -654,17 +758,29 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     return s;
 }
 
-hipError_t launch_attend(const AttendArgs& a, const AttendShape& sh, int64_t channels, bool fp8, hipStream_t s) {
+template <int D>
+hipError_t launch_channels(const AttendArgs& a, const AttendShape& sh, bool fp8, hipStream_t s) {
+    if (a.page_tokens % 16 == 0) return fp8 ? launch<D, true, true>(a, sh, s) : launch<D, false, true>(a, sh, s);
+    return fp8 ? launch<D, true, false>(a, sh, s) : launch<D, false, false>(a, sh, s);
+}
+
+hipError_t launch_attend(const AttendArgs& args, const AttendShape& sh, int64_t channels, bool fp8, hipStream_t s) {
+    AttendArgs a = args;
+    // t / page_tokens = t page_mul >> page_shift for t < 2^31: page_mul = ceil(2^(31 + e) / page_tokens) with
+    // 2^e >= page_tokens exceeds the quotient by less than 2^e / 2^(31 + e) parts of a page a token
+    uint32_t e = 0;
+    while ((uint64_t(1) << e) < a.page_tokens) ++e;
+    a.page_shift = 31 + e;
+    a.page_mul = static_cast<uint32_t>(((uint64_t(1) << a.page_shift) + a.page_tokens - 1) / a.page_tokens);
     if (a.rows == 0) {                          // nothing to compute, but the outcome
-        AttendArgs none = a;
-        k_attend<64, false, 1><<<1, 64 * kWaves, 0, s>>>(none);
+        k_attend<64, false, 1, false><<<1, 64 * kWaves, 0, s>>>(a);
         return hipGetLastError();
     }
     switch (channels) {
-        case 64: return fp8 ? launch<64, true>(a, sh, s) : launch<64, false>(a, sh, s);
-        case 128: return fp8 ? launch<128, true>(a, sh, s) : launch<128, false>(a, sh, s);
-        case 192: return fp8 ? launch<192, true>(a, sh, s) : launch<192, false>(a, sh, s);
-        case 256: return fp8 ? launch<256, true>(a, sh, s) : launch<256, false>(a, sh, s);
+        case 64: return launch_channels<64>(a, sh, fp8, s);
+        case 128: return launch_channels<128>(a, sh, fp8, s);
+        case 192: return launch_channels<192>(a, sh, fp8, s);
+        case 256: return launch_channels<256>(a, sh, fp8, s);
         default: return hipErrorInvalidValue;
     }
 }

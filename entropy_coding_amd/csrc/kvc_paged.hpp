@@ -94,6 +94,7 @@ struct AttendArgs {
     const int32_t* block_table;
     int64_t max_pages, num_pages;
     uint32_t page_tokens, heads, batch, ratio;
+    uint32_t page_mul, page_shift;      // t / page_tokens as a product (launch_attend sets them)
     const uint16_t* q;
     int64_t q_row, q_head;
     uint16_t* out;
@@ -113,6 +114,6 @@ struct AttendArgs {
 };
 AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t channels, bool fp8, int64_t rows,
                          int64_t rows_per_sequence, int64_t max_tokens);
-hipError_t launch_attend(const AttendArgs& a, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& args, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
 
 }  // namespace kvc
