@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
 ARCH = os.environ.get("KVC_OFFLOAD_ARCH", "gfx950")
 
-KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip"]
+KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip", "kvc_attention_wide.hip"]
 HOST = ["kvc_api.cpp", "kvc_paged_api.cpp"]
 
 COMMON = [

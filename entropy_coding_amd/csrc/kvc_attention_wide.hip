@@ -1,0 +1,382 @@
+// Attention of drafted tokens over a paged cache for sequences with more than
+// 16 query rows a KV head (trees, pieces of a prompt).  The mathematics and the
+// operands' layouts are those of kvc_attention.hip; here the four waves of a
+// workgroup hold different rows (16 RT each) and walk the same tokens, tiles of
+// 64 of which they stage in LDS together, so that K and V are read from memory,
+// widened from e4m3 and transposed once for 64 RT rows.
+//
+// LDS holds a tile as the matrix instruction's operands, 1 KB each, lane after
+// lane: K in 4 x D / 32 of them (16 tokens x 32 channels), V^T in 2 x D / 16
+// (16 channels x 32 tokens).  Writes and reads are 16 bytes a lane in lane
+// order, free of bank conflicts.  Waves 0 and 1 stage 32 tokens of K each,
+// waves 2 and 3 of V.  Two tiles fit: the next one is on its way from memory to
+// registers while the current one is multiplied, and is written beside it
+// before the one barrier of a tile.
+#include "kvc_attend_device.hpp"
+
+namespace kvc {
+namespace {
+
+constexpr int kWideTile = 64;
+
+// Workgroups (of a wave a SIMD) that a CU can hold at once: by the registers
+// of a wave (sums, queries, scores, weights, the staged quarter of a tile and
+// about 70 for the rest, of 512) and by two tiles of 160 KB of LDS.
+constexpr int groups_of(int d, bool fp8, int rt) {
+    const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 64;
+    const int regs = need <= 168 ? 3 : need <= 256 ? 2 : 1;
+    const int fit = 160 * 1024 / (2 * kWideTile * d * 4 + 256);
+    return regs < fit ? regs : fit;
+}
+
+template <int D>
+struct WideLds {
+    u32x4 k[2][4 * (D / 32)][64];
+    u32x4 v[2][2 * (D / 16)][64];
+};
+
+// PAGE4: pages are a multiple of 4 tokens, so that a run of four V rows lies
+// in one.
+template <int D, bool FP8, int RT, bool PAGE4>
+__global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_wide(AttendArgs a) {
+    constexpr int C = D / 16;                   // channels of V a lane stages
+    constexpr int ES = FP8 ? 1 : 2;
+    constexpr int VW = C * ES / 4;              // words of them
+    constexpr int KG = D * ES / 64;             // 16-byte pieces of K a lane stages of one token
+    constexpr int KK = D / 32;                  // products over the channels
+    constexpr int N4 = 2 * KG;                  // 16-byte registers a lane stages, of K or of V
+    constexpr int VS = PAGE4 ? 2 : 8;
+    __shared__ WideLds<D> lds;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
+    const bool is_v = wave >= 2;
+    const uint32_t place = place_of(blockIdx.x, gridDim.x);
+    const Plan plan = plan_of(a, 1);
+    uint32_t bad_page = 0;
+    const uint32_t from = place * plan.per, end = from + plan.per;
+    uint32_t at = from;
+    bool note = blockIdx.x == 0 && wave == 0;
+    while (at < end) {
+        const Share sh = share_of(a, plan, at, note);
+        note = false;
+        if (!sh.any) break;
+        const Part pt = part_of(a, sh, place, at, from, end, kWideTile);
+        at = sh.first + sh.units;               // the next item's first unit
+        const int length = pt.length, ctx = pt.context, ta = pt.ta, tb = pt.tb;
+        const int row0 = pt.row0 + wave * 16 * RT;
+        const bool active = row0 < pt.rows;
+
+        const uint32_t row_bytes = a.heads * D * ES;
+        const GlobalBytes pool =
+            reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[is_v])) + sh.head * (D * ES);
+        const int32_t* const table = a.block_table + int64_t(sh.b) * a.max_pages;
+
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+        bf16x8 qf[RT][KK];
+        int node[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const Query query(a, sh, row0 + rt * 16 + n, pt.rows);
+            node[rt] = query.node;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                qf[rt][kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, flip);
+        }
+        f32x4 o[RT][C];
+        float mx[RT], l[RT];                    // mx: of the scores before their scale
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            mx[rt] = kNegInf;
+            l[rt] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[rt][c] = f32x4{0, 0, 0, 0};
+        }
+
+        // Staging.  A wave has 32 tokens of a tile: a lane of K token n of both halves, a lane of V a run of four of
+        // each half.  Page numbers are read a tile ahead of the rows.
+        const int half32 = (wave & 1) * 32;
+        auto token = [&](int t, int i) -> uint32_t {
+            const int x = t * kWideTile + half32 + (is_v ? (VS == 2 ? 16 * i : (i < 4 ? 0 : 12) + i) + q4 * 4 : 16 * (i & 1) + n);
+            return static_cast<uint32_t>(x < length ? x : VS == 2 && is_v ? (length - 1) & ~3 : length - 1);
+        };
+        int32_t page[VS];
+        auto read_pages = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < VS; ++i) page[i] = table[page_index(a, token(t, i))];
+        };
+        u32x4 st[N4];
+        auto load = [&](int t) {
+            if (is_v) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = VS == 2 ? j / 4 : j;
+                    const uint32_t slot = slot_in(a, page[i], token(t, i), &bad_page) + (VS == 2 ? j & 3 : 0);
+                    Words<VW> w;
+                    w.load(pool + uint64_t(slot) * row_bytes + n * (C * ES));
+#pragma unroll
+                    for (int x = 0; x < VW; ++x) st[(j * VW + x) / 4][(j * VW + x) % 4] = w[x];
+                }
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const GlobalBytes p =
+                        pool + uint64_t(slot_in(a, page[hf], token(t, hf), &bad_page)) * row_bytes + 16 * q4;
+#pragma unroll
+                    for (int kg = 0; kg < KG; ++kg)
+                        st[hf * KG + kg] = *reinterpret_cast<const KVC_GLOBAL u32x4*>(p + 64 * kg);
+                }
+            }
+        };
+        bool any_wild = false;
+        auto write = [&](int t, int buf) {
+            if (is_v) {
+                const int t0 = t * kWideTile + half32;
+                if (t0 + 32 > ctx) {
+                    // tokens behind the last one are cleared, and infinities and NaN of drafted ones
+                    uint32_t wild = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int tok = t0 + (j < 4 ? 0 : 12) + q4 * 4 + j;
+                        const uint32_t there = tok < length ? ~0u : 0u, drafted = tok >= ctx ? ~0u : 0u;
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) {
+                            uint32_t w = st[(j * VW + x) / 4][(j * VW + x) % 4] & there;
+                            const uint32_t bits = wild_bits<FP8>(w) & drafted;
+                            wild |= bits;
+                            if (drafted) w = without_wild<FP8>(w);
+                            st[(j * VW + x) / 4][(j * VW + x) % 4] = w;
+                        }
+                    }
+                    any_wild = any_wild || __any(wild != 0);
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    u32x4 f;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int x = 2 * p * VW + c * ES / 4, y = x + VW;
+                        f[p] = pair_of<FP8>(st[x / 4][x % 4], st[y / 4][y % 4], c);
+                    }
+                    lds.v[buf][(wave & 1) * C + c][lane] = f;
+                }
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int kg = 0; kg < KG; ++kg) {
+                        const u32x4 x = st[hf * KG + kg];
+                        u32x4* const to = &lds.k[buf][((wave & 1) * 2 + hf) * KK + kg * (FP8 ? 2 : 1)][lane];
+                        if constexpr (FP8) {
+                            to[0] = u32x4{widen<false>(x[0]), widen<true>(x[0]), widen<false>(x[1]), widen<true>(x[1])};
+                            to[64] = u32x4{widen<false>(x[2]), widen<true>(x[2]), widen<false>(x[3]), widen<true>(x[3])};
+                        } else {
+                            to[0] = x;
+                        }
+                    }
+            }
+        };
+
+        auto compute = [&](int t, int buf) {
+            const int t0 = t * kWideTile;
+            f32x4 s[RT][4];
+#pragma unroll
+            for (int hf = 0; hf < 4; ++hf) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) s[rt][hf] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const bf16x8 kf = __builtin_bit_cast(bf16x8, lds.k[buf][hf * KK + kk][lane]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        s[rt][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][kk], s[rt][hf], 0, 0, 0);
+                }
+            }
+            // (operands are not read ahead of the phase that uses them: their registers are)
+            __builtin_amdgcn_sched_barrier(0xF);
+            if (t0 + kWideTile > pt.full) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const uint64_t win = window_of(a, sh.seq.start, node[rt], t0 - ctx, length - ctx) >> (q4 * 4);
+#pragma unroll
+                    for (int hf = 0; hf < 4; ++hf)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((win >> (hf * 16 + i)) & 1u)) s[rt][hf][i] = kNegInf;
+                }
+            }
+            float zero[RT];
+            bool grows = false;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float top = fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3]));
+#pragma unroll
+                for (int hf = 1; hf < 4; ++hf)
+                    top = fmaxf(fmaxf(top, fmaxf(s[rt][hf][0], s[rt][hf][1])), fmaxf(s[rt][hf][2], s[rt][hf][3]));
+                top = fmaxf(top_of_column(top), mx[rt]);
+                grows = grows || top > mx[rt];
+                zero[rt] = top;
+            }
+            if (__any(grows)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float f = __builtin_amdgcn_exp2f((mx[rt] - (zero[rt] == kNegInf ? 0.0f : zero[rt])) * scale);
+                    mx[rt] = zero[rt];
+                    l[rt] *= f;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) o[rt][c] *= f;
+                }
+            }
+            bf16x8 pf[RT][2];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float shift = zero[rt] == kNegInf ? 0.0f : -zero[rt] * scale;
+#pragma unroll
+                for (int st2 = 0; st2 < 2; ++st2) {
+                    float e[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][2 * st2 + (j >> 2)][j & 3], scale, shift));
+                    l[rt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                    pf[rt][st2] = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0xF);
+#pragma unroll
+            for (int st2 = 0; st2 < 2; ++st2)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const bf16x8 vf = __builtin_bit_cast(bf16x8, lds.v[buf][st2 * C + c][lane]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        o[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][st2], o[rt][c], 0, 0, 0);
+                }
+        };
+
+        if (ta < tb) {
+            read_pages(ta);
+            load(ta);
+            read_pages(ta + 1);
+            write(ta, 0);
+            __syncthreads();
+            for (int t = ta; t < tb; ++t) {
+                const int buf = (t - ta) & 1;
+                if (t + 1 < tb) {
+                    load(t + 1);
+                    read_pages(t + 2);
+                }
+                if (active) compute(t, buf);
+                if (t + 1 < tb) write(t + 1, buf ^ 1);
+                __syncthreads();
+            }
+        }
+        any_wild = __syncthreads_or(any_wild);
+
+        // each wave has its rows' sums: lane l those of row n, channels 4 q C .. 4 (q + 1) C - 1
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            l[rt] += __shfl_xor(l[rt], 16);
+            l[rt] += __shfl_xor(l[rt], 32);
+            const int m = row0 + rt * 16 + n;
+            if (m < pt.rows) {
+                const float best = mx[rt] * scale;
+                const float sum = l[rt];
+                if (pt.whole) {
+                    const int64_t row = int64_t(sh.seq.start) + node[rt];
+                    const int64_t head = int64_t(sh.head) * a.ratio + (m - node[rt] * static_cast<int>(a.ratio));
+                    const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+                    uint16_t* const out = a.out + row * a.out_row + head * D + q4 * 4 * C;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < C; c += 4)
+                            *reinterpret_cast<uint2*>(out + i * C + c) =
+                                uint2{two_bf16(o[rt][c][i] * inv, o[rt][c + 1][i] * inv),
+                                      two_bf16(o[rt][c + 2][i] * inv, o[rt][c + 3][i] * inv)};
+                    if (a.lse && q4 == 0)
+                        a.lse[row * (int64_t(a.heads) * a.ratio) + head] =
+                            sum == 0.0f ? kNegInf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
+                } else {
+                    const uint64_t to = (uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0);
+                    float* const out = a.partial + to * D + q4 * 4 * C;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < C; c += 4)
+                            *reinterpret_cast<f32x4*>(out + i * C + c) =
+                                f32x4{o[rt][c][i], o[rt][c + 1][i], o[rt][c + 2][i], o[rt][c + 3][i]};
+                    if (q4 == 0) *reinterpret_cast<float2*>(a.pairs + 2 * to) = float2{best, sum};
+                }
+            }
+        }
+        if (any_wild) {
+            // Rare: added to what this lane has just written.
+            const GlobalBytes vp =
+                reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[1])) + sh.head * (D * ES);
+            const int last = tb * kWideTile < length ? tb * kWideTile : length;
+            for (int m = row0 + n; m < pt.rows && m < row0 + 16 * RT; m += 16) {
+                const int nd = m / static_cast<int>(a.ratio);
+                const int64_t row = int64_t(sh.seq.start) + nd;
+                const int64_t head = int64_t(sh.head) * a.ratio + (m - nd * static_cast<int>(a.ratio));
+                uint16_t* const out = a.out + row * a.out_row + head * D + q4 * 4 * C;
+                float* const part = a.partial + ((uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0)) * D + q4 * 4 * C;
+                for (int tok = ta * kWideTile > ctx ? ta * kWideTile : ctx; tok < last; ++tok) {
+                    if (!sees(a, sh.seq.start, nd, static_cast<uint32_t>(tok - ctx))) continue;
+                    uint32_t known = 0;
+                    const GlobalBytes p =
+                        vp + uint64_t(slot_in(a, table[page_index(a, tok)], tok, &known)) * row_bytes + q4 * 4 * (C * ES);
+                    for (int c = 0; c < 4 * C; ++c) {
+                        const uint32_t w = *reinterpret_cast<const KVC_GLOBAL uint32_t*>(p + 4 * (c * ES / 4));
+                        const float x = wild_part<FP8>(w, c);
+                        if (x == 0.0f) continue;
+                        if (pt.whole) out[c] = static_cast<uint16_t>(two_bf16(__uint_as_float(uint32_t(out[c]) << 16) + x, 0.0f));
+                        else part[c] += x;
+                    }
+                }
+            }
+        }
+    }
+    const uint32_t any = __syncthreads_or(static_cast<int>(bad_page));
+    if (threadIdx.x == 0) a.words[blockIdx.x] = any ? kPagedInvalid : 0u;
+}
+
+template <int D, bool FP8, bool PAGE4>
+hipError_t launch(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
+    switch (sh.row_tiles) {
+        case 1: k_attend_wide<D, FP8, 1, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
+        case 2:
+            if constexpr (D <= 192) k_attend_wide<D, FP8, 2, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+            else return hipErrorInvalidValue;
+            break;
+        default:
+            if constexpr (D <= 128) k_attend_wide<D, FP8, 4, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+            else return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_channels(const AttendArgs& a, const AttendShape& sh, bool fp8, hipStream_t s) {
+    if (a.page_tokens % 4 == 0) return fp8 ? launch<D, true, true>(a, sh, s) : launch<D, false, true>(a, sh, s);
+    return fp8 ? launch<D, true, false>(a, sh, s) : launch<D, false, false>(a, sh, s);
+}
+
+}  // namespace
+
+int wide_groups(int64_t channels, bool fp8, int row_tiles) {
+    return groups_of(static_cast<int>(channels), fp8, row_tiles);
+}
+
+hipError_t launch_attend_wide(const AttendArgs& a, const AttendShape& sh, int64_t channels, bool fp8, hipStream_t s) {
+    switch (channels) {
+        case 64: return launch_channels<64>(a, sh, fp8, s);
+        case 128: return launch_channels<128>(a, sh, fp8, s);
+        case 192: return launch_channels<192>(a, sh, fp8, s);
+        case 256: return launch_channels<256>(a, sh, fp8, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace kvc

@@ -66,25 +66,29 @@ hipError_t launch_append(const AppendArgs& a, bool rounds, hipStream_t s);
 // ---- attention
 
 // Head of the workspace; behind it one AttendSpan a sequence, then a word a
-// workgroup (not 0: it met a page number outside the pool), then the partial
-// outputs and their (maximum, sum) pairs, each part 256-byte aligned.
+// workgroup (not 0: it met a page number outside the pool), then the (maximum,
+// sum) pairs and the sums of V of the parts, two parts a workgroup, each
+// region 256-byte aligned.
 struct AttendControl {
     uint32_t magic;
     uint32_t flags;                     // kPagedInvalid: a sequence that does not fit
     uint32_t grid;
     uint32_t words_offset;
+    uint32_t per;                       // units a workgroup takes
 };
-struct AttendSpan {                     // where a sequence's partials lie
-    uint32_t base;                      // its first workgroup
-    uint32_t splits;                    // 0: none of its rows is computed
-    uint32_t tiles;                     // row tiles
+struct AttendSpan {                     // a sequence on the line of units
+    uint32_t base;                      // its first unit
+    uint32_t units;                     // of each of its items
+    uint32_t tiles;                     // row tiles; 0: none of its rows is computed
     uint32_t pad;
 };
 
 struct AttendShape {                    // what the launch is made for
-    int row_tiles;                      // 16-row tiles a workgroup holds
-    uint32_t target;                    // workgroups that fill the chip
-    uint32_t grid;
+    bool wide;                          // rows over the waves (kvc_attention_wide.hip), not tokens
+    int row_tiles;                      // 16-row tiles a wave holds
+    uint32_t tile_shift;                // 2^tile_shift rows of a workgroup
+    uint32_t unit_shift;                // 2^unit_shift tokens of a unit of work
+    uint32_t grid;                      // workgroups; where items may be split: that fill the chip
     bool split;                         // whether a sequence may be split
     uint64_t spans, words, partial, pairs, total;   // workspace offsets and size
 };
@@ -93,7 +97,9 @@ struct AttendArgs {
     void* const* pools;                 // the layer's K pool, then its V pool
     const int32_t* block_table;
     int64_t max_pages, num_pages;
+    int32_t max_tokens;                 // that the table has room for, < 2^31 - 255
     uint32_t page_tokens, heads, batch, ratio;
+    uint32_t tile_shift, unit_shift;    // of the shape
     uint32_t page_mul, page_shift;      // t / page_tokens as a product (launch_attend sets them)
     const uint16_t* q;
     int64_t q_row, q_head;
@@ -105,7 +111,7 @@ struct AttendArgs {
     const uint64_t* mask;
     uint32_t mask_words, rows;
     float scale_log2, v_scale;
-    uint32_t target, split;
+    uint32_t target, split;             // workgroups to deal units to; 0: an item a workgroup
     AttendControl* ctl;
     AttendSpan* spans;
     uint32_t* words;
@@ -113,7 +119,9 @@ struct AttendArgs {
     float* pairs;                       // (maximum, sum) each
 };
 AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t channels, bool fp8, int64_t rows,
-                         int64_t rows_per_sequence, int64_t max_tokens);
+                         int64_t rows_per_sequence, int64_t max_tokens, int64_t widest);
 hipError_t launch_attend(const AttendArgs& args, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
+hipError_t launch_attend_wide(const AttendArgs& a, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
+int wide_groups(int64_t channels, bool fp8, int row_tiles);     // workgroups of it that a CU holds
 
 }  // namespace kvc

@@ -74,7 +74,7 @@ kvc::AttendShape shape_of(const kvc_paged_kv* g, const kvc_attention* p) {
     const int64_t widest = g->max_pages * int64_t(g->page_tokens);
     const int64_t longest = p->max_tokens > 0 && p->max_tokens < widest ? p->max_tokens : widest;
     return kvc::attend_shape(g->batch, g->heads, p->q_heads / g->heads, p->channels, p->kv_dtype == KVC_E4M3, p->rows,
-                             p->rows_per_sequence, longest);
+                             p->rows_per_sequence, longest, widest);
 }
 
 }  // namespace
@@ -180,6 +180,10 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
     a.block_table = h_paged->d_block_table;
     a.max_pages = h_paged->max_pages;
     a.num_pages = h_paged->num_pages;
+    const int64_t room = h_paged->max_pages * int64_t(h_paged->page_tokens);
+    a.max_tokens = static_cast<int32_t>(room < 0x7FFFFF00 ? room : 0x7FFFFF00);
+    a.tile_shift = shape.tile_shift;
+    a.unit_shift = shape.unit_shift;
     a.page_tokens = h_paged->page_tokens;
     a.heads = static_cast<uint32_t>(h_paged->heads);
     a.batch = static_cast<uint32_t>(h_paged->batch);
@@ -197,7 +201,7 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
     a.rows = static_cast<uint32_t>(p->rows);
     a.scale_log2 = static_cast<float>(double(p->softmax_scale) * double(p->k_scale) * 1.4426950408889634);
     a.v_scale = p->v_scale;
-    a.target = shape.target;
+    a.target = shape.grid;
     a.split = shape.split;
     a.ctl = static_cast<kvc::AttendControl*>(d_workspace);
     a.spans = reinterpret_cast<kvc::AttendSpan*>(ws + shape.spans);
