@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "kvc_paged.hpp"
+#include "kvc_wave.hpp"
 
 namespace kvc {
 
@@ -34,24 +35,6 @@ __device__ inline Seq seq_of(const AttendArgs& a, uint32_t b) {
             s.context > a.max_tokens || end - s.start > a.max_tokens - s.context;
     s.rows = s.bad ? 0 : end - s.start;
     return s;
-}
-
-// Sums over a wave's lanes, without the trip through LDS that a shuffle
-// takes: of the lanes up to this one, and of all.
-template <int CTRL, int ROWS>
-__device__ uint32_t add_moved(uint32_t x) {
-    return x + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false));
-}
-__device__ inline uint32_t scan(uint32_t x) {
-    x = add_moved<0x111, 0xF>(x);               // within rows of 16 lanes: from 1, 2, 4 and 8 lanes before
-    x = add_moved<0x112, 0xF>(x);
-    x = add_moved<0x114, 0xF>(x);
-    x = add_moved<0x118, 0xF>(x);
-    x = add_moved<0x142, 0xA>(x);               // the last lane of the row before, into rows 1 and 3
-    return add_moved<0x143, 0xC>(x);            // lane 31 into rows 2 and 3
-}
-__device__ inline uint32_t of_lane(uint32_t x, int lane) {
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
 }
 
 // The work of a call as a line of units.  Sequence b has heads x tiles_b
@@ -97,8 +80,8 @@ __device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
     units = of_lane(scan(units), 63);
     p.aligned = items <= a.target / 2;
     const uint32_t over = p.aligned ? a.target - items : a.target;
-    // whole rounds of the waves that take one unit each (least: a power of two)
-    p.per = ((units + over - 1) / over + least - 1) & ~(least - 1);
+
+    p.per = (units + over - 1) / over;
     if (p.per < least) p.per = least;
     return p;
 }
@@ -223,12 +206,23 @@ __device__ inline uint32_t two_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
-// The largest of the four lanes n, n + 16, n + 32, n + 48.
-__device__ inline float top_of_column(float x) {
+// The larger one, NaN if one is: three at a time are one instruction, while
+// the maximum that prefers numbers needs its arguments quieted first.
+__device__ inline float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+__device__ inline float larger(float top, f32x4 x) { return larger(larger(larger(larger(top, x[0]), x[1]), x[2]), x[3]); }
+
+// The largest of the four lanes n, n + 16, n + 32, n + 48, and of y.
+__device__ inline float top_of_column(float x, float y) {
     u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    x = larger(__uint_as_float(r[0]), __uint_as_float(r[1]));
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    return larger(larger(__uint_as_float(r[0]), __uint_as_float(r[1])), y);
+}
+
+// Words read through the scalar cache: they are not written while the kernel
+// runs, and every lane wants the same ones.
+__device__ inline int32_t uniform_word(const int32_t* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
 }
 
 // ---------------------------------------------------------------- infinities and NaN

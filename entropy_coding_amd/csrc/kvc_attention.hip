@@ -41,12 +41,6 @@ struct Lds {
     float m[kWaves][16], l[kWaves][16];
 };
 
-// Words read through the scalar cache: they are not written while the kernel
-// runs, and every lane wants the same ones.
-__device__ int32_t uniform_word(const int32_t* p) {
-    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
-}
-
 // Waves that a SIMD can hold at once, from the registers that a wave needs:
 // queries, a tile of K and of V, the sums, and about 80 for the rest, of 512
 // (fewer waves rather than registers kept in memory).
@@ -224,9 +218,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
             }
 
             // weights 2^(scale (s - max))
-            float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                              fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-            top = fmaxf(top_of_column(top), mx);
+            // (a NaN among the scores a row sees makes its maximum, its weights and its sums NaN)
+            const float top = top_of_column(larger(larger(kNegInf, s[0]), s[1]), mx);
             const float zero = top == kNegInf ? 0.0f : top;
             if (__any(top > mx)) {
                 const float f = __builtin_amdgcn_exp2f((mx - zero) * scale);
@@ -494,12 +487,7 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
 
 hipError_t launch_attend(const AttendArgs& args, const AttendShape& sh, int64_t channels, bool fp8, hipStream_t s) {
     AttendArgs a = args;
-    // t / page_tokens = t page_mul >> page_shift for t < 2^31: page_mul = ceil(2^(31 + e) / page_tokens) with
-    // 2^e >= page_tokens exceeds the quotient by less than 2^e / 2^(31 + e) parts of a page a token
-    uint32_t e = 0;
-    while ((uint64_t(1) << e) < a.page_tokens) ++e;
-    a.page_shift = 31 + e;
-    a.page_mul = static_cast<uint32_t>(((uint64_t(1) << a.page_shift) + a.page_tokens - 1) / a.page_tokens);
+    set_page_product(a.page_tokens, &a.page_mul, &a.page_shift);
     if (a.rows == 0) {                          // nothing to compute, but the outcome
         k_attend<64, false, 1><<<1, 64 * kWaves, 0, s>>>(a);
         return hipGetLastError();

@@ -35,9 +35,10 @@ struct WideLds {
     u32x4 v[2][2 * (D / 16)][64];
 };
 
-// PAGE4: pages are a multiple of 4 tokens, so that a run of four V rows lies
-// in one.
-template <int D, bool FP8, int RT, bool PAGE4>
+// PAGE: 16, 4 or 1, the largest that divides the tokens of a page: with 16 a
+// half of a wave's 32 tokens lies in one page, its rows a constant stride
+// apart; with 4 a lane's run of four V rows does.
+template <int D, bool FP8, int RT, int PAGE>
 __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_wide(AttendArgs a) {
     constexpr int C = D / 16;                   // channels of V a lane stages
     constexpr int ES = FP8 ? 1 : 2;
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     constexpr int KG = D * ES / 64;             // 16-byte pieces of K a lane stages of one token
     constexpr int KK = D / 32;                  // products over the channels
     constexpr int N4 = 2 * KG;                  // 16-byte registers a lane stages, of K or of V
-    constexpr int VS = PAGE4 ? 2 : 8;
+    constexpr int VS = PAGE == 1 ? 8 : 2;
     __shared__ WideLds<D> lds;
 
     const int lane = threadIdx.x & 63;
@@ -99,31 +100,39 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         // each half.  Page numbers are read a tile ahead of the rows.
         const int half32 = (wave & 1) * 32;
         auto token = [&](int t, int i) -> uint32_t {
-            const int x = t * kWideTile + half32 + (is_v ? (VS == 2 ? 16 * i : (i < 4 ? 0 : 12) + i) + q4 * 4 : 16 * (i & 1) + n);
-            return static_cast<uint32_t>(x < length ? x : VS == 2 && is_v ? (length - 1) & ~3 : length - 1);
+            const int x = t * kWideTile + half32 +
+                          (PAGE == 16 ? 16 * i : is_v ? (VS == 2 ? 16 * i : (i < 4 ? 0 : 12) + i) + q4 * 4 : 16 * (i & 1) + n);
+            return static_cast<uint32_t>(x < length ? x : PAGE == 16 ? (length - 1) & ~15
+                                                          : PAGE == 4 && is_v ? (length - 1) & ~3 : length - 1);
         };
         int32_t page[VS];
         auto read_pages = [&](int t) {
 #pragma unroll
-            for (int i = 0; i < VS; ++i) page[i] = table[page_index(a, token(t, i))];
+            for (int i = 0; i < VS; ++i) {
+                const int32_t* const at_page = table + page_index(a, token(t, i));
+                page[i] = PAGE == 16 ? uniform_word(at_page) : *at_page;
+            }
+        };
+        auto row_at = [&](int t, int i) -> uint64_t {
+            return uint64_t(slot_in(a, page[i], token(t, i), &bad_page)) * row_bytes;
         };
         u32x4 st[N4];
         auto load = [&](int t) {
             if (is_v) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int i = VS == 2 ? j / 4 : j;
-                    const uint32_t slot = slot_in(a, page[i], token(t, i), &bad_page) + (VS == 2 ? j & 3 : 0);
+                    const GlobalBytes p = pool + row_at(t, VS == 2 ? j / 4 : j) +
+                                          ((PAGE == 16 ? q4 * 4 + (j & 3) : PAGE == 4 ? j & 3 : 0) * row_bytes +
+                                           uint32_t(n) * (C * ES));
                     Words<VW> w;
-                    w.load(pool + uint64_t(slot) * row_bytes + n * (C * ES));
+                    w.load(p);
 #pragma unroll
                     for (int x = 0; x < VW; ++x) st[(j * VW + x) / 4][(j * VW + x) % 4] = w[x];
                 }
             } else {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const GlobalBytes p =
-                        pool + uint64_t(slot_in(a, page[hf], token(t, hf), &bad_page)) * row_bytes + 16 * q4;
+                    const GlobalBytes p = pool + row_at(t, hf) + ((PAGE == 16 ? n * row_bytes : 0u) + 16u * q4);
 #pragma unroll
                     for (int kg = 0; kg < KG; ++kg)
                         st[hf * KG + kg] = *reinterpret_cast<const KVC_GLOBAL u32x4*>(p + 64 * kg);
@@ -211,13 +220,11 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             bool grows = false;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                float top = fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3]));
+                float top = kNegInf;
 #pragma unroll
-                for (int hf = 1; hf < 4; ++hf)
-                    top = fmaxf(fmaxf(top, fmaxf(s[rt][hf][0], s[rt][hf][1])), fmaxf(s[rt][hf][2], s[rt][hf][3]));
-                top = fmaxf(top_of_column(top), mx[rt]);
-                grows = grows || top > mx[rt];
-                zero[rt] = top;
+                for (int hf = 0; hf < 4; ++hf) top = larger(top, s[rt][hf]);
+                zero[rt] = top_of_column(top, mx[rt]);
+                grows = grows || zero[rt] > mx[rt];
             }
             if (__any(grows)) {
 #pragma unroll
@@ -342,25 +349,24 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     if (threadIdx.x == 0) a.words[blockIdx.x] = any ? kPagedInvalid : 0u;
 }
 
-template <int D, bool FP8, bool PAGE4>
+template <int D, bool FP8, int PAGE>
 hipError_t launch(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
-    switch (sh.row_tiles) {
-        case 1: k_attend_wide<D, FP8, 1, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a); break;
-        case 2:
-            if constexpr (D <= 192) k_attend_wide<D, FP8, 2, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a);
-            else return hipErrorInvalidValue;
-            break;
-        default:
-            if constexpr (D <= 128) k_attend_wide<D, FP8, 4, PAGE4><<<sh.grid, 64 * kWaves, 0, s>>>(a);
-            else return hipErrorInvalidValue;
+    if (sh.row_tiles == 1) {
+        k_attend_wide<D, FP8, 1, PAGE><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    if constexpr (D <= 192) {
+        k_attend_wide<D, FP8, 2, PAGE><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
 }
 
 template <int D>
 hipError_t launch_channels(const AttendArgs& a, const AttendShape& sh, bool fp8, hipStream_t s) {
-    if (a.page_tokens % 4 == 0) return fp8 ? launch<D, true, true>(a, sh, s) : launch<D, false, true>(a, sh, s);
-    return fp8 ? launch<D, true, false>(a, sh, s) : launch<D, false, false>(a, sh, s);
+    if (a.page_tokens % 16 == 0) return fp8 ? launch<D, true, 16>(a, sh, s) : launch<D, false, 16>(a, sh, s);
+    if (a.page_tokens % 4 == 0) return fp8 ? launch<D, true, 4>(a, sh, s) : launch<D, false, 4>(a, sh, s);
+    return fp8 ? launch<D, true, 1>(a, sh, s) : launch<D, false, 1>(a, sh, s);
 }
 
 }  // namespace

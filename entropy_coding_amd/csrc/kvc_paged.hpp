@@ -14,6 +14,16 @@ enum : uint32_t {
     kPagedCapacity = 2u,
 };
 
+// t / page_tokens = t mul >> shift for t < 2^31: mul = ceil(2^(31 + e) /
+// page_tokens) with 2^e >= page_tokens exceeds the quotient by less than
+// 2^e / 2^(31 + e) parts of a page a token.
+inline void set_page_product(uint32_t page_tokens, uint32_t* mul, uint32_t* shift) {
+    uint32_t e = 0;
+    while ((uint64_t(1) << e) < page_tokens) ++e;
+    *shift = 31 + e;
+    *mul = static_cast<uint32_t>(((uint64_t(1) << *shift) + page_tokens - 1) / page_tokens);
+}
+
 // ---- block tables
 
 // Head of the workspace; behind it (at kTableArraysOffset) three int32
@@ -33,6 +43,7 @@ inline __host__ __device__ int64_t table_array(int64_t batch) { return (batch + 
 struct TableArgs {
     int64_t batch, max_pages, num_pages, free_capacity, max_rows;
     uint32_t page_tokens, trim;
+    uint32_t page_mul, page_shift;      // t / page_tokens as a product (the launch sets them)
     const int32_t* cached;
     const int32_t* fresh;
     const int32_t* held_in;
@@ -47,7 +58,7 @@ struct TableArgs {
     TableControl* ctl;
     int32_t* arrays;
 };
-hipError_t launch_block_table(const TableArgs& a, hipStream_t s);
+hipError_t launch_block_table(const TableArgs& args, hipStream_t s);
 
 // ---- append
 
@@ -100,7 +111,7 @@ struct AttendArgs {
     int32_t max_tokens;                 // that the table has room for, < 2^31 - 255
     uint32_t page_tokens, heads, batch, ratio;
     uint32_t tile_shift, unit_shift;    // of the shape
-    uint32_t page_mul, page_shift;      // t / page_tokens as a product (launch_attend sets them)
+    uint32_t page_mul, page_shift;      // t / page_tokens as a product (the launch sets them)
     const uint16_t* q;
     int64_t q_row, q_head;
     uint16_t* out;
