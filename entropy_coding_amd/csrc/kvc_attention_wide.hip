@@ -1,7 +1,8 @@
 // Attention of drafted tokens over a paged cache for sequences with more than
 // 16 query rows a KV head (trees, pieces of a prompt).  The mathematics and the
 // operands' layouts are those of kvc_attention.hip; here the four waves of a
-// workgroup hold different rows (16 RT each) and walk the same tokens, tiles of
+// workgroup hold different rows (RT groups of 16, dealt to the waves in turn, so
+// that few rows keep four SIMDs busy) and walk the same tokens, tiles of
 // 64 of which they stage in LDS together, so that K and V are read from memory,
 // widened from e4m3 and transposed once for 64 RT rows.
 //
@@ -14,16 +15,21 @@
 // before the one barrier of a tile.
 #include "kvc_attend_device.hpp"
 
+#include <type_traits>
+
 namespace kvc {
 namespace {
 
 constexpr int kWideTile = 64;
 
+constexpr int kAhead = 4;
+constexpr int kNoDs = 0x7F;                     // the scheduler may move all across but LDS instructions
+
 // Workgroups (of a wave a SIMD) that a CU can hold at once: by the registers
 // of a wave (sums, queries, scores, weights, the staged quarter of a tile and
-// about 70 for the rest, of 512) and by two tiles of 160 KB of LDS.
+// about 80 for the rest, of 512) and by two tiles of 160 KB of LDS.
 constexpr int groups_of(int d, bool fp8, int rt) {
-    const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 64;
+    const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 80;
     const int regs = need <= 168 ? 3 : need <= 256 ? 2 : 1;
     const int fit = 160 * 1024 / (2 * kWideTile * d * 4 + 256);
     return regs < fit ? regs : fit;
@@ -66,8 +72,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         const Part pt = part_of(a, sh, place, at, from, end, kWideTile);
         at = sh.first + sh.units;               // the next item's first unit
         const int length = pt.length, ctx = pt.context, ta = pt.ta, tb = pt.tb;
-        const int row0 = pt.row0 + wave * 16 * RT;
-        const bool active = row0 < pt.rows;
+        const int row0 = pt.row0 + wave * 16;   // of this wave's first group; the others are 64 apart
+        const int groups = row0 < pt.rows ? (pt.rows - row0 + 63) / 64 : 0;
 
         const uint32_t row_bytes = a.heads * D * ES;
         const GlobalBytes pool =
@@ -80,7 +86,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         int node[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const Query query(a, sh, row0 + rt * 16 + n, pt.rows);
+            const Query query(a, sh, row0 + rt * 64 + n, pt.rows);
             node[rt] = query.node;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
@@ -188,26 +194,29 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             }
         };
 
-        auto compute = [&](int t, int buf) {
+        auto compute = [&](int t, int buf, auto held) {
+            constexpr int G = held;             // groups that have rows
             const int t0 = t * kWideTile;
-            f32x4 s[RT][4];
+            // Operands are read from LDS kAhead before their products: one by one, each pair of products would wait for
+            // a whole trip to LDS.
+            u32x4 ring[kAhead];
 #pragma unroll
-            for (int hf = 0; hf < 4; ++hf) {
+            for (int i = 0; i < kAhead; ++i) ring[i] = lds.k[buf][i][lane];
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 s[G][4];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) s[rt][hf] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 4 * KK; ++i) {
+                const int hf = i / KK, kk = i % KK;
+                const bf16x8 kf = __builtin_bit_cast(bf16x8, ring[i % kAhead]);
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const bf16x8 kf = __builtin_bit_cast(bf16x8, lds.k[buf][hf * KK + kk][lane]);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        s[rt][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][kk], s[rt][hf], 0, 0, 0);
-                }
+                for (int rt = 0; rt < G; ++rt)
+                    s[rt][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][kk], kk ? s[rt][hf] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+                if (i + kAhead < 4 * KK) ring[i % kAhead] = lds.k[buf][i + kAhead][lane];
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // (operands are not read ahead of the phase that uses them: their registers are)
-            __builtin_amdgcn_sched_barrier(0xF);
             if (t0 + kWideTile > pt.full) {
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
+                for (int rt = 0; rt < G; ++rt) {
                     const uint64_t win = window_of(a, sh.seq.start, node[rt], t0 - ctx, length - ctx) >> (q4 * 4);
 #pragma unroll
                     for (int hf = 0; hf < 4; ++hf)
@@ -216,10 +225,10 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                             if (!((win >> (hf * 16 + i)) & 1u)) s[rt][hf][i] = kNegInf;
                 }
             }
-            float zero[RT];
+            float zero[G];
             bool grows = false;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
+            for (int rt = 0; rt < G; ++rt) {
                 float top = kNegInf;
 #pragma unroll
                 for (int hf = 0; hf < 4; ++hf) top = larger(top, s[rt][hf]);
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             }
             if (__any(grows)) {
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
+                for (int rt = 0; rt < G; ++rt) {
                     const float f = __builtin_amdgcn_exp2f((mx[rt] - (zero[rt] == kNegInf ? 0.0f : zero[rt])) * scale);
                     mx[rt] = zero[rt];
                     l[rt] *= f;
@@ -236,12 +245,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                     for (int c = 0; c < C; ++c) o[rt][c] *= f;
                 }
             }
-            bf16x8 pf[RT][2];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float shift = zero[rt] == kNegInf ? 0.0f : -zero[rt] * scale;
+            for (int i = 0; i < kAhead; ++i) ring[i] = lds.v[buf][i][lane];
+            __builtin_amdgcn_sched_barrier(kNoDs);
+            bf16x8 pf[G][2];
 #pragma unroll
-                for (int st2 = 0; st2 < 2; ++st2) {
+            for (int st2 = 0; st2 < 2; ++st2) {
+#pragma unroll
+                for (int rt = 0; rt < G; ++rt) {
+                    const float shift = zero[rt] == kNegInf ? 0.0f : -zero[rt] * scale;
                     float e[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -250,16 +262,16 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                     pf[rt][st2] = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
                 }
             }
-            __builtin_amdgcn_sched_barrier(0xF);
 #pragma unroll
-            for (int st2 = 0; st2 < 2; ++st2)
+            for (int i = 0; i < 2 * C; ++i) {
+                const int st2 = i / C, c = i % C;
+                const bf16x8 vf = __builtin_bit_cast(bf16x8, ring[i % kAhead]);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const bf16x8 vf = __builtin_bit_cast(bf16x8, lds.v[buf][st2 * C + c][lane]);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        o[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][st2], o[rt][c], 0, 0, 0);
-                }
+                for (int rt = 0; rt < G; ++rt)
+                    o[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][st2], o[rt][c], 0, 0, 0);
+                if (i + kAhead < 2 * C) ring[i % kAhead] = lds.v[buf][i + kAhead][lane];
+                __builtin_amdgcn_sched_barrier(kNoDs);
+            }
         };
 
         if (ta < tb) {
@@ -274,7 +286,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                     load(t + 1);
                     read_pages(t + 2);
                 }
-                if (active) compute(t, buf);
+                if (RT == 2 && groups > 1) compute(t, buf, std::integral_constant<int, RT>{});
+                else if (groups) compute(t, buf, std::integral_constant<int, 1>{});
                 if (t + 1 < tb) write(t + 1, buf ^ 1);
                 __syncthreads();
             }
@@ -286,7 +299,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         for (int rt = 0; rt < RT; ++rt) {
             l[rt] += __shfl_xor(l[rt], 16);
             l[rt] += __shfl_xor(l[rt], 32);
-            const int m = row0 + rt * 16 + n;
+            const int m = row0 + rt * 64 + n;
             if (m < pt.rows) {
                 const float best = mx[rt] * scale;
                 const float sum = l[rt];
@@ -323,7 +336,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             const GlobalBytes vp =
                 reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[1])) + sh.head * (D * ES);
             const int last = tb * kWideTile < length ? tb * kWideTile : length;
-            for (int m = row0 + n; m < pt.rows && m < row0 + 16 * RT; m += 16) {
+            for (int m = row0 + n; m < pt.rows && m < row0 + 64 * RT; m += 64) {
                 const int nd = m / static_cast<int>(a.ratio);
                 const int64_t row = int64_t(sh.seq.start) + nd;
                 const int64_t head = int64_t(sh.head) * a.ratio + (m - nd * static_cast<int>(a.ratio));
