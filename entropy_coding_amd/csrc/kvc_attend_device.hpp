@@ -44,10 +44,10 @@ __device__ inline Seq seq_of(const AttendArgs& a, uint32_t b) {
 // workgroup has the same number of units, whatever the lengths, and leaves at
 // most two parts of items that others share: the end of one that began before
 // its range (part 2 w) and the beginning of one that ends behind it (2 w + 1).
-// With few items (half as many as workgroups, or fewer) the units of an item
-// are rounded up to a multiple of `per` instead, so that no workgroup works
-// on two: total + items x per <= workgroups x per still holds.  Every wave
-// finds its place from the lengths (no launch of its own for a plan, nothing
+// Where the units of each item can be rounded up to a multiple of `per`, or
+// of an eighth more, and still fit the workgroups, they are: then none works
+// on two items (few long ones, or many of one length).  Every wave finds its
+// place from the lengths (no launch of its own for a plan, nothing
 // kept between calls).  unit_shift is such that the units of a call whose row
 // starts are prefix sums stay below 2^31; where they are not, sums may wrap,
 // and what a workgroup takes for its share still lies within one sequence.
@@ -68,21 +68,30 @@ __device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
     Plan p{1, false};
     if (!a.split) return p;                     // an item a workgroup
     const uint32_t lane = threadIdx.x & 63;
-    uint32_t units = 0, items = 0;
-    for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
-        if (b0 + lane < a.batch) {
-            const Seq s = seq_of(a, b0 + lane);
-            items += Plan::tiles(a, s) * a.heads;
-            units += Plan::tiles(a, s) * a.heads * Plan::real(a, s);
-        }
+    // the first 64 sequences' items and units, kept for all sums
+    uint32_t items0 = 0, real0 = 0;
+    if (lane < a.batch) {
+        const Seq s = seq_of(a, lane);
+        items0 = Plan::tiles(a, s) * a.heads;
+        real0 = Plan::real(a, s);
     }
-    items = of_lane(scan(items), 63);
-    units = of_lane(scan(units), 63);
-    p.aligned = items <= a.target / 2;
-    const uint32_t over = p.aligned ? a.target - items : a.target;
-
-    p.per = (units + over - 1) / over;
-    if (p.per < least) p.per = least;
+    auto sum = [&](auto of_item) {              // over all items, of what their units give
+        uint32_t x = items0 * of_item(real0);
+        for (uint32_t b = 64 + lane; b < a.batch; b += 64) {
+            const Seq s = seq_of(a, b);
+            x += Plan::tiles(a, s) * a.heads * of_item(Plan::real(a, s));
+        }
+        return of_lane(scan(x), 63);
+    };
+    const uint32_t units = sum([](uint32_t real) { return real; });
+    uint32_t per = (units + a.target - 1) / a.target;
+    if (per < least) per = least;
+    p.per = per;
+    for (int i = 0; i < 2 && !p.aligned; ++i, per += (per + 7) / 8) {
+        if (sum([&](uint32_t real) { return (real + per - 1) / per; }) > a.target) continue;
+        p.aligned = true;
+        p.per = per;
+    }
     return p;
 }
 
@@ -211,13 +220,56 @@ __device__ inline uint32_t two_bf16(float lo, float hi) {
 __device__ inline float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
 __device__ inline float larger(float top, f32x4 x) { return larger(larger(larger(larger(top, x[0]), x[1]), x[2]), x[3]); }
 
-// The largest of the four lanes n, n + 16, n + 32, n + 48, and of y.
-__device__ inline float top_of_column(float x, float y) {
+// A row's weights are 2^(scale s - m) with m the largest scaled score when it
+// was last set: it is set anew only when a score passes it by kSlack, so that
+// the sums are rarely rescaled (with every new largest score, some row of a
+// wave would be at every other tile of a long sequence).  Weights up to
+// 2^kSlack lose nothing in floating point.
+constexpr float kSlack = 8.0f;
+
+// The largest of the four lanes n, n + 16, n + 32, n + 48.
+__device__ inline float top_of_column(float x) {
     u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = larger(__uint_as_float(r[0]), __uint_as_float(r[1]));
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return larger(larger(__uint_as_float(r[0]), __uint_as_float(r[1])), y);
+    return larger(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+
+// A row's reference m (as -m, what a weight's exponent adds to the scaled
+// score), the score that sets it anew, and the sum of its weights.
+struct RowSum {
+    float shift = 0.0f, limit = kNegInf, sum = 0.0f;
+
+    __device__ float top() const { return limit == kNegInf ? kNegInf : -shift; }
+
+    // Sets m to the largest of the column where that passes the limit; returns what the sums are multiplied with.
+    __device__ float raise(float top, float scale, float slack) {
+        top = top_of_column(top);
+        if (!(top > limit)) return 1.0f;
+        const float now = -top * scale;
+        const float f = limit == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(now - shift);
+        shift = now;
+        limit = top + slack;
+        sum *= f;
+        return f;
+    }
+};
+
+// The scale of the scores as a positive number, the same for all lanes (a
+// scale of zero becomes the smallest one), and the bits that the queries'
+// values take for its sign: so the largest scaled score is the scaled largest.
+struct Scale {
+    float scale, slack;
+    uint32_t flip;
+
+    __device__ explicit Scale(const AttendArgs& a) {
+        const uint32_t bits = __builtin_amdgcn_readfirstlane(__float_as_uint(a.scale_log2));
+        flip = (bits >> 31) ? 0x80008000u : 0u;
+        const uint32_t size = bits & 0x7FFFFFFFu;
+        scale = __uint_as_float(size < 0x00800000u ? 0x00800000u : size);
+        slack = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(kSlack / scale)));
+    }
+};
 
 // Words read through the scalar cache: they are not written while the kernel
 // runs, and every lane wants the same ones.

@@ -66,6 +66,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
     const int n = lane & 15, q4 = lane >> 4;
     const uint32_t place = place_of(blockIdx.x, gridDim.x);
     const Plan plan = plan_of(a, kWaves);
+    const Scale sc(a);
     uint32_t bad_page = 0;
     const uint32_t from = place * plan.per, end = from + plan.per;
     uint32_t at = from;
@@ -83,18 +84,15 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
         const GlobalBytes vp = reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[1])) + sh.head * (D * ES);
         const int32_t* const table = a.block_table + int64_t(sh.b) * a.max_pages;
 
-        // The query rows, as the second operand of K Q^T.  The scale is made positive by their sign, so that the
-        // largest scaled score is the scaled largest score; a scale of zero becomes the smallest one.
-        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+        // the query rows, as the second operand of K Q^T
         const Query query(a, sh, pt.row0 + n, pt.rows);
         bf16x8 qf[KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
-            qf[kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, flip);
+            qf[kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, sc.flip);
 
         f32x4 o[C];
-        float mx = kNegInf, l = 0.0f;           // mx: of the scores before their scale
+        RowSum row;
 #pragma unroll
         for (int c = 0; c < C; ++c) o[c] = f32x4{0, 0, 0, 0};
 
@@ -217,22 +215,17 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
                 }
             }
 
-            // weights 2^(scale (s - max))
-            // (a NaN among the scores a row sees makes its maximum, its weights and its sums NaN)
-            const float top = top_of_column(larger(larger(kNegInf, s[0]), s[1]), mx);
-            const float zero = top == kNegInf ? 0.0f : top;
-            if (__any(top > mx)) {
-                const float f = __builtin_amdgcn_exp2f((mx - zero) * scale);
-                l *= f;
+            // weights (a NaN among the scores a row sees makes them and its sums NaN)
+            const float top = larger(larger(kNegInf, s[0]), s[1]);
+            if (__any(top > row.limit)) {
+                const float f = row.raise(top, sc.scale, sc.slack);
 #pragma unroll
                 for (int c = 0; c < C; ++c) o[c] *= f;
-                mx = top;
             }
-            const float shift = -zero * scale;
             float e[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 2][j & 3], scale, shift));
-            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j >> 2][j & 3], sc.scale, row.shift));
+            row.sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
             const bf16x8 pf = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
 
             // the weighted sum of V, one product for each of a lane's channels
@@ -270,8 +263,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
             }
         }
 
-        // the four waves' sums, joined through LDS; from here on the maxima are of the scaled scores
-        mx *= scale;
+        // the four waves' sums, joined through LDS
+        const float mx = row.top();
+        float l = row.sum;
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (q4 == 0) {
@@ -318,16 +312,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
                 }
             }
             if (pt.whole) {
-                const int64_t row = int64_t(sh.seq.start) + node;
+                const int64_t out_row = int64_t(sh.seq.start) + node;
                 const int64_t head = int64_t(sh.head) * a.ratio + g;
                 const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-                uint16_t* const out = a.out + row * a.out_row + head * D + part * C;
+                uint16_t* const out = a.out + out_row * a.out_row + head * D + part * C;
 #pragma unroll
                 for (int i = 0; i < C / 4; ++i)
                     *reinterpret_cast<uint2*>(out + 4 * i) =
                         uint2{two_bf16(acc[i][0] * inv, acc[i][1] * inv), two_bf16(acc[i][2] * inv, acc[i][3] * inv)};
                 if (a.lse && part == 0)
-                    a.lse[row * (int64_t(a.heads) * a.ratio) + head] =
+                    a.lse[out_row * (int64_t(a.heads) * a.ratio) + head] =
                         sum == 0.0f ? kNegInf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
             } else {
                 const uint64_t to = uint64_t(pt.slot) * 16 + lr;
@@ -466,7 +460,7 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     s.wide = usual > 16;
     s.row_tiles = !s.wide || usual <= 64 || channels > 192 ? 1 : 2;
     s.tile_shift = !s.wide ? 4 : s.row_tiles == 1 ? 6 : s.row_tiles == 2 ? 7 : 8;
-    s.split = max_tokens > 128;
+    s.split = max_tokens > (s.wide ? 512 : 1024);
     // every sequence's rows fill whole tiles but the last one
     const uint64_t tile_rows = uint64_t(1) << s.tile_shift;
     const uint64_t items = uint64_t(heads) * (uint64_t(rows) * ratio / tile_rows + (rows < batch ? rows : batch));

@@ -61,6 +61,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     const bool is_v = wave >= 2;
     const uint32_t place = place_of(blockIdx.x, gridDim.x);
     const Plan plan = plan_of(a, 1);
+    const Scale sc(a);
     uint32_t bad_page = 0;
     const uint32_t from = place * plan.per, end = from + plan.per;
     uint32_t at = from;
@@ -80,8 +81,6 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[is_v])) + sh.head * (D * ES);
         const int32_t* const table = a.block_table + int64_t(sh.b) * a.max_pages;
 
-        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
         bf16x8 qf[RT][KK];
         int node[RT];
 #pragma unroll
@@ -90,17 +89,14 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             node[rt] = query.node;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                qf[rt][kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, flip);
+                qf[rt][kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, sc.flip);
         }
         f32x4 o[RT][C];
-        float mx[RT], l[RT];                    // mx: of the scores before their scale
+        RowSum row[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            mx[rt] = kNegInf;
-            l[rt] = 0.0f;
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int c = 0; c < C; ++c) o[rt][c] = f32x4{0, 0, 0, 0};
-        }
 
         // Staging.  A wave has 32 tokens of a tile: a lane of K token n of both halves, a lane of V a run of four of
         // each half.  Page numbers are read a tile ahead of the rows.
@@ -197,6 +193,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         auto compute = [&](int t, int buf, auto held) {
             constexpr int G = held;             // groups that have rows
             const int t0 = t * kWideTile;
+            __builtin_amdgcn_s_setprio(1);
             // Operands are read from LDS kAhead before their products: one by one, each pair of products would wait for
             // a whole trip to LDS.
             u32x4 ring[kAhead];
@@ -225,22 +222,20 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                             if (!((win >> (hf * 16 + i)) & 1u)) s[rt][hf][i] = kNegInf;
                 }
             }
-            float zero[G];
+            __builtin_amdgcn_s_setprio(0);
+            float top[G];
             bool grows = false;
 #pragma unroll
             for (int rt = 0; rt < G; ++rt) {
-                float top = kNegInf;
+                top[rt] = kNegInf;
 #pragma unroll
-                for (int hf = 0; hf < 4; ++hf) top = larger(top, s[rt][hf]);
-                zero[rt] = top_of_column(top, mx[rt]);
-                grows = grows || zero[rt] > mx[rt];
+                for (int hf = 0; hf < 4; ++hf) top[rt] = larger(top[rt], s[rt][hf]);
+                grows = grows || top[rt] > row[rt].limit;
             }
             if (__any(grows)) {
 #pragma unroll
                 for (int rt = 0; rt < G; ++rt) {
-                    const float f = __builtin_amdgcn_exp2f((mx[rt] - (zero[rt] == kNegInf ? 0.0f : zero[rt])) * scale);
-                    mx[rt] = zero[rt];
-                    l[rt] *= f;
+                    const float f = row[rt].raise(top[rt], sc.scale, sc.slack);
 #pragma unroll
                     for (int c = 0; c < C; ++c) o[rt][c] *= f;
                 }
@@ -253,12 +248,11 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             for (int st2 = 0; st2 < 2; ++st2) {
 #pragma unroll
                 for (int rt = 0; rt < G; ++rt) {
-                    const float shift = zero[rt] == kNegInf ? 0.0f : -zero[rt] * scale;
                     float e[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][2 * st2 + (j >> 2)][j & 3], scale, shift));
-                    l[rt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][2 * st2 + (j >> 2)][j & 3], sc.scale, row[rt].shift));
+                    row[rt].sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
                     pf[rt][st2] = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
                 }
             }
@@ -297,17 +291,17 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         // each wave has its rows' sums: lane l those of row n, channels 4 q C .. 4 (q + 1) C - 1
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            l[rt] += __shfl_xor(l[rt], 16);
-            l[rt] += __shfl_xor(l[rt], 32);
+            float sum = row[rt].sum;
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
             const int m = row0 + rt * 64 + n;
             if (m < pt.rows) {
-                const float best = mx[rt] * scale;
-                const float sum = l[rt];
+                const float best = row[rt].top();
                 if (pt.whole) {
-                    const int64_t row = int64_t(sh.seq.start) + node[rt];
+                    const int64_t out_row = int64_t(sh.seq.start) + node[rt];
                     const int64_t head = int64_t(sh.head) * a.ratio + (m - node[rt] * static_cast<int>(a.ratio));
                     const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-                    uint16_t* const out = a.out + row * a.out_row + head * D + q4 * 4 * C;
+                    uint16_t* const out = a.out + out_row * a.out_row + head * D + q4 * 4 * C;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -316,7 +310,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
                                 uint2{two_bf16(o[rt][c][i] * inv, o[rt][c + 1][i] * inv),
                                       two_bf16(o[rt][c + 2][i] * inv, o[rt][c + 3][i] * inv)};
                     if (a.lse && q4 == 0)
-                        a.lse[row * (int64_t(a.heads) * a.ratio) + head] =
+                        a.lse[out_row * (int64_t(a.heads) * a.ratio) + head] =
                             sum == 0.0f ? kNegInf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
                 } else {
                     const uint64_t to = (uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0);
@@ -338,9 +332,9 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             const int last = tb * kWideTile < length ? tb * kWideTile : length;
             for (int m = row0 + n; m < pt.rows && m < row0 + 64 * RT; m += 64) {
                 const int nd = m / static_cast<int>(a.ratio);
-                const int64_t row = int64_t(sh.seq.start) + nd;
+                const int64_t out_row = int64_t(sh.seq.start) + nd;
                 const int64_t head = int64_t(sh.head) * a.ratio + (m - nd * static_cast<int>(a.ratio));
-                uint16_t* const out = a.out + row * a.out_row + head * D + q4 * 4 * C;
+                uint16_t* const out = a.out + out_row * a.out_row + head * D + q4 * 4 * C;
                 float* const part = a.partial + ((uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0)) * D + q4 * 4 * C;
                 for (int tok = ta * kWideTile > ctx ? ta * kWideTile : ctx; tok < last; ++tok) {
                     if (!sees(a, sh.seq.start, nd, static_cast<uint32_t>(tok - ctx))) continue;
