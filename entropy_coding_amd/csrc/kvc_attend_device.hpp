@@ -152,6 +152,7 @@ __device__ inline Share share_of(const AttendArgs& a, const Plan& p, uint32_t at
             a.ctl->words_offset =
                 static_cast<uint32_t>(reinterpret_cast<char*>(a.words) - reinterpret_cast<char*>(a.ctl));
             a.ctl->per = p.per;
+            a.ctl->aligned = p.aligned;
         }
     }
     r.head = __builtin_amdgcn_readfirstlane(r.head);

@@ -396,37 +396,46 @@ struct Joined {
     }
 };
 
+// each: (row, query head) pairs of a wave, one after the other.
 template <int D>
-__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, uint32_t grid) {
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, uint32_t grid, uint32_t each) {
     constexpr int E = D / 64;
     const uint32_t lane = threadIdx.x & 63;
     const uint32_t heads = a.heads * a.ratio;
-    const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-    const uint32_t row = id / heads, head = id - row * heads;
-    if (row >= a.rows) return;
+    const uint32_t first_id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)) * each;
     const uint32_t per = a.ctl->per;
-    const uint32_t b = sequence_of(a.row_starts, a.batch, row, lane);
-    const int32_t start = a.row_starts[b], next = a.row_starts[b + 1];
-    const AttendSpan span = a.spans[b];
-    if (static_cast<int32_t>(row) < start || static_cast<int32_t>(row) >= next) return;
-    const uint32_t h = head / a.ratio, m = (row - static_cast<uint32_t>(start)) * a.ratio + (head - h * a.ratio);
-    const uint32_t tile = m >> a.tile_shift;
-    if (tile >= span.tiles) return;
-    const uint32_t first = span.base + (h * span.tiles + tile) * span.units;
-    const uint32_t w0 = first / per, w1 = (first + span.units - 1) / per;
-    if (w0 >= w1 || w1 >= grid) return;
-    const uint32_t parts = w1 - w0 + 1;
-    const uint32_t lr = m - (tile << a.tile_shift);
-    auto place = [&](uint32_t s) { return (uint64_t(2 * (w0 + s) + (s ? 0 : 1)) << a.tile_shift) + lr; };
-    Joined<D> j;
-    if (parts <= 4) j.template add<4>(a, lane, parts, place);
-    else j.template add<E <= 2 ? 16 : 8>(a, lane, parts, place);
-    const float inv = j.sum == 0.0f ? 0.0f : a.v_scale / j.sum;
-    uint16_t* const out = a.out + int64_t(row) * a.out_row + int64_t(head) * D + lane * E;
+    const bool aligned = a.ctl->aligned;
+    int32_t start = 0, next = 0;                // of the sequence that `span` is of
+    AttendSpan span{};
+    uint32_t row = first_id / heads, head = first_id - row * heads;
+    for (uint32_t i = 0; i < each && row < a.rows; ++i, head = head + 1 < heads ? head + 1 : 0, row += head ? 0 : 1) {
+        if (static_cast<int32_t>(row) >= next) {
+            const uint32_t b = sequence_of(a.row_starts, a.batch, row, lane);
+            start = a.row_starts[b];
+            next = a.row_starts[b + 1];
+            span = a.spans[b];
+        }
+        // (outside any sequence, or of one whose items nobody shares)
+        if (static_cast<int32_t>(row) < start || static_cast<int32_t>(row) >= next || (aligned && span.units <= per)) continue;
+        const uint32_t h = head / a.ratio, m = (row - static_cast<uint32_t>(start)) * a.ratio + (head - h * a.ratio);
+        const uint32_t tile = m >> a.tile_shift;
+        if (tile >= span.tiles) continue;
+        const uint32_t first = span.base + (h * span.tiles + tile) * span.units;
+        const uint32_t w0 = first / per, w1 = (first + span.units - 1) / per;
+        if (w0 >= w1 || w1 >= grid) continue;
+        const uint32_t parts = w1 - w0 + 1;
+        const uint32_t lr = m - (tile << a.tile_shift);
+        auto place = [&](uint32_t s) { return (uint64_t(2 * (w0 + s) + (s ? 0 : 1)) << a.tile_shift) + lr; };
+        Joined<D> j;
+        if (parts <= 4) j.template add<4>(a, lane, parts, place);
+        else j.template add<E <= 2 ? 16 : 8>(a, lane, parts, place);
+        const float inv = j.sum == 0.0f ? 0.0f : a.v_scale / j.sum;
+        uint16_t* const out = a.out + int64_t(row) * a.out_row + int64_t(head) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(j.o[e] * inv));
-    if (a.lse && lane == 0)
-        a.lse[int64_t(row) * heads + head] = j.sum == 0.0f ? kNegInf : (j.top + __builtin_amdgcn_logf(j.sum)) * kLn2;
+        for (int e = 0; e < E; ++e) out[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(j.o[e] * inv));
+        if (a.lse && lane == 0)
+            a.lse[int64_t(row) * heads + head] = j.sum == 0.0f ? kNegInf : (j.top + __builtin_amdgcn_logf(j.sum)) * kLn2;
+    }
 }
 
 template <int D>
@@ -445,8 +454,11 @@ hipError_t launch_channels(const AttendArgs& a, const AttendShape& sh, bool fp8,
         else k_attend<D, false, 1><<<sh.grid, 64 * kWaves, 0, s>>>(a);
     }
     if (sh.split) {
-        const uint64_t waves = uint64_t(a.rows) * a.heads * a.ratio;
-        k_attend_join<D><<<static_cast<uint32_t>((waves + 3) / 4), 256, 0, s>>>(a, sh.grid);
+        // at most as many waves as the chip holds at once: where nothing was split, more of them than that only to
+        // find it out cost a prompt of 2000 rows 15 us
+        const uint64_t pairs = uint64_t(a.rows) * a.heads * a.ratio;
+        const uint64_t each = (pairs + 8191) / 8192, waves = (pairs + each - 1) / each;
+        k_attend_join<D><<<static_cast<uint32_t>((waves + 3) / 4), 256, 0, s>>>(a, sh.grid, static_cast<uint32_t>(each));
     }
     return hipGetLastError();
 }

@@ -86,6 +86,7 @@ struct AttendControl {
     uint32_t grid;
     uint32_t words_offset;
     uint32_t per;                       // units a workgroup takes
+    uint32_t aligned;                   // items begin at multiples of it
 };
 struct AttendSpan {                     // a sequence on the line of units
     uint32_t base;                      // its first unit
