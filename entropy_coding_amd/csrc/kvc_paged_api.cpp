@@ -59,11 +59,13 @@ bool attention_sizes_ok(const kvc_paged_kv* g, const kvc_attention* p) {
 bool attention_ok(const kvc_paged_kv* g, const kvc_attention* p) {
     if (!attention_sizes_ok(g, p) || !g->d_block_table || !aligned(g->d_block_table, 4)) return false;
     if (p->rows > 0 && (!p->d_q || !p->d_out || !aligned(p->d_q, 16) || !aligned(p->d_out, 16))) return false;
-    const int64_t out_row = p->q_heads * p->channels;
-    if (p->q_row_stride % 8 || p->q_head_stride % 8 || p->out_row_stride % 8 || p->q_row_stride < 0 ||
-        p->q_head_stride < 0 || p->q_row_stride > kMaxScalars || p->q_head_stride > kMaxScalars ||
-        p->out_row_stride > kMaxScalars || (p->rows > 1 && p->out_row_stride < out_row))
+    // (strides between one row, or one head, say nothing)
+    const auto stride_ok = [](int64_t stride, int64_t least) {
+        return stride >= least && stride <= kMaxScalars && stride % 8 == 0;
+    };
+    if (p->rows > 1 && (!stride_ok(p->q_row_stride, 0) || !stride_ok(p->out_row_stride, p->q_heads * p->channels)))
         return false;
+    if (p->q_heads > 1 && !stride_ok(p->q_head_stride, 0)) return false;
     if (!p->d_row_starts || !aligned(p->d_row_starts, 4) || !aligned(p->d_context_lens, 4) || !aligned(p->d_lse, 4) ||
         !aligned(p->d_tree_mask, 8))
         return false;
@@ -144,8 +146,7 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
     const int64_t width = h_paged->heads * channels;
     if (!d_k || !d_v || !d_slots || !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_slots, 8)) return KVC_ERR_INVALID;
     for (int64_t stride : {k_row_stride, v_row_stride})
-        if (stride < 0 || stride > kMaxScalars || (stride * size) % 16 || (rows > 1 && stride < width))
-            return KVC_ERR_INVALID;
+        if (rows > 1 && (stride < width || stride > kMaxScalars || (stride * size) % 16)) return KVC_ERR_INVALID;
     kvc::AppendArgs a;
     a.pools = h_paged->d_pools + 2 * layer;
     a.k = d_k;
@@ -153,8 +154,8 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
     a.slots = d_slots;
     a.rows = rows;
     a.n_slots = h_paged->num_pages * int64_t(h_paged->page_tokens);
-    a.k_stride = k_row_stride * size;
-    a.v_stride = v_row_stride * size;
+    a.k_stride = rows > 1 ? k_row_stride * size : 0;
+    a.v_stride = rows > 1 ? v_row_stride * size : 0;
     a.row_bytes = static_cast<uint32_t>(width * value_bytes(kv_dtype));
     a.k_scale = k_scale;
     a.v_scale = v_scale;
@@ -189,10 +190,10 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
     a.batch = static_cast<uint32_t>(h_paged->batch);
     a.ratio = static_cast<uint32_t>(p->q_heads / h_paged->heads);
     a.q = static_cast<const uint16_t*>(p->d_q);
-    a.q_row = p->q_row_stride;
-    a.q_head = p->q_head_stride;
+    a.q_row = p->rows > 1 ? p->q_row_stride : 0;
+    a.q_head = p->q_heads > 1 ? p->q_head_stride : 0;
     a.out = static_cast<uint16_t*>(p->d_out);
-    a.out_row = p->out_row_stride;
+    a.out_row = p->rows > 1 ? p->out_row_stride : 0;
     a.lse = p->d_lse;
     a.row_starts = p->d_row_starts;
     a.context = p->d_context_lens;

@@ -520,6 +520,11 @@ def _tensor(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
 
 
+def _rows_contiguous(t):
+    """Whether the values of each t[i] [heads, channels] lie one after the other."""
+    return t.numel() == 0 or t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
+
+
 def _queue(device, stream, call, *tensors):
     """Runs call(stream pointer) with `device` current, on `stream` (the
     device's current one if None), and keeps the tensors' memory until the
@@ -618,7 +623,7 @@ def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tenso
     _tensor(slots, "slots", torch.int64, (None,), dev)
     heads, ch = paged.desc.heads, paged.channels
     for t, name in ((k, "k"), (v, "v")):
-        if t.device != dev or t.shape != (rows, heads, ch) or (rows and t.stride()[1:] != (ch, 1)) or t.dtype != k.dtype:
+        if t.device != dev or t.shape != (rows, heads, ch) or not _rows_contiguous(t) or t.dtype != k.dtype:
             raise ValueError(f"{name} must be [{rows}, {heads}, {ch}] on {dev}, a row's values contiguous")
     st = _queue(dev, stream,
                 lambda s: _lib_append(paged.ref, layer, paged.kv_dtype, ch, k.data_ptr(), v.data_ptr(), _kv_dtype(k),
@@ -673,8 +678,7 @@ class PagedAttention:
             with torch.cuda.stream(stream):
                 out = torch.empty((rows, self.q_heads, ch), dtype=q.dtype, device=dev) if out is None else out
                 lse = torch.empty((rows, self.q_heads), dtype=torch.float32, device=dev) if lse is None else lse
-        if out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or \
-                (rows and out.stride()[1:] != (ch, 1)):
+        if out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or not _rows_contiguous(out):
             raise ValueError(f"out must be bf16 {list(q.shape)} on {dev}, a row's values contiguous")
         _tensor(lse, "lse", torch.float32, (rows, self.q_heads), dev)
         d.d_q, d.q_row_stride, d.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)

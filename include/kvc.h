@@ -453,7 +453,7 @@ int kvc_block_table_result(const void* d_workspace, void* stream, int64_t* h_row
  * saturated, NaN kept.  Scales are finite and positive, and 1 when the types
  * are the same.  h_paged as for kvc_decode_paged (its table is not read and
  * may be NULL).  d_k and d_v 16-byte aligned, row strides (in values, at
- * least heads x channels when rows > 1) such that every row is.  Does not
+ * least heads x channels; not looked at for one row) such that every row is.  Does not
  * synchronise; KVC_ERR_INVALID for bad arguments, nothing launched.
  */
 int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtype, int64_t channels,
@@ -476,9 +476,9 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  *     lse = log sum_t e^(s_t);
  * a row that sees nothing has o = 0 and lse = -infinity.  What K or V hold
  * (NaN, infinity) at tokens that a row does not see has no part in it.  Sums,
- * maxima and the output's accumulation are float32; the weights e^(s - max)
- * are rounded to bf16 for the matrix instructions (see the kernel), the
- * output to bf16.  Rows behind d_row_starts[batch] are left as they were.
+ * maxima and the output's accumulation are float32; the weights are rounded
+ * to bf16 for the matrix instructions, the output to bf16.  Rows behind
+ * d_row_starts[batch] are left as they were.
  * q and out bf16, the cache bf16 or e4m3; channels 64, 128, 192 or 256;
  * q_heads a multiple of heads, at most 1024 per KV head.  num_pages x
  * page_tokens < 2^31.
@@ -486,15 +486,16 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * depend on them: the usual n_b (0: rows / batch) and the longest context +
  * n_b (0: max_pages x page_tokens).
  * Does not synchronise.  kvc_paged_attention_result gives KVC_ERR_INVALID
- * where row starts fall or pass `rows`, a context is negative, a sequence
- * passes max_pages x page_tokens tokens (that sequence's rows are not
- * written), or a page number read lies outside [0, num_pages) (page 0 is
+ * where a sequence's row starts fall or pass `rows`, its context is negative
+ * or it passes max_pages x page_tokens tokens (that sequence's rows are not
+ * written), or where a page number read lies outside [0, num_pages) (page 0 is
  * read in its place: its rows are undefined).
  * Workspace: kvc_paged_attention_sizes, 256-byte aligned.
  */
 typedef struct kvc_attention {
     const void* d_q;                /* [rows][q_heads][channels] bf16                 */
-    int64_t q_row_stride;           /* in values, multiples of 8                      */
+    int64_t q_row_stride;           /* in values, multiples of 8 (a stride between one
+                                       row or one head is not looked at)              */
     int64_t q_head_stride;
     void* d_out;                    /* [rows][q_heads][channels] bf16                 */
     int64_t out_row_stride;         /* in values, multiples of 8; heads are channels apart */

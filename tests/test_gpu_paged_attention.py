@@ -338,3 +338,51 @@ def test_function_form_and_argument_checks(kvc, cuda):
         kvc.PagedAttention(c.paged(), 5, 6)
     with pytest.raises(kvc.KvcError):
         kvc.PagedAttention(c.paged(), 4, 6, k_scale=0.0)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 4.0])
+@pytest.mark.parametrize("nodes", [[1, 2], [20, 9]])
+def test_scales(kvc, cuda, scale, nodes):
+    """Negative, zero, vanishing and large softmax scales."""
+    c = Case(kvc, cuda, [300, 77], nodes, 2, 2, 64, "bf16", 16, True, seed=20, scale=scale)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("gain", [0.02, 0.3, 3.0])
+@pytest.mark.parametrize("nodes", [[1, 3], [40, 21]])
+def test_scores_that_grow_along_the_sequence(kvc, cuda, kind, gain, nodes):
+    """Maxima that are passed by little, at every token, and by much: keys
+    that point more and more along (or against) one direction that the
+    queries share."""
+    c = Case(kvc, cuda, [1500, 200], nodes, 1, 4, 128, kind, 16, False, seed=21, scale=1.0)
+    one = torch.zeros(128, device=cuda)
+    one[5] = 1.0
+    for b in range(2):
+        total = int(c.contexts[b] + c.nodes[b])
+        t = torch.arange(total, device=cuda)
+        slot = torch.from_numpy(c.table[b]).to(cuda).long()[t // 16] * 16 + t % 16
+        k = c.pools[2 * c.layer].view(torch.int16 if kind == "bf16" else torch.uint8).view(-1, 1, 128)
+        step = (t if b == 0 else total - t).float() * gain / 10
+        rows = (step.clamp(max=400)[:, None, None] * one).to(KIND[kind])
+        k[slot] = rows.view(k.dtype)
+    c.q = (one + 0.01 * c.q.float()).to(torch.bfloat16)
+    c.check(c.run())
+
+
+def test_more_sequences_than_lanes_and_long_ones_among_them(kvc, cuda):
+    rng = np.random.default_rng(22)
+    contexts, nodes = rng.integers(0, 60, 200), rng.integers(0, 3, 200)
+    contexts[[3, 66, 199]], nodes[[3, 66, 199]] = [7000, 3000, 5000], [25, 1, 30]
+    c = Case(kvc, cuda, contexts, nodes, 1, 2, 64, "bf16", 16, True, seed=23)
+    ref = c.ref()
+    c.check(c.run(), ref)
+    c.check(c.run(hint=30), ref)
+
+
+def test_one_row_or_one_head_of_any_stride(kvc, cuda):
+    c = Case(kvc, cuda, [20], [1], 1, 1, 64, "bf16", 16, False, seed=24)
+    ref = c.ref()
+    wide = torch.zeros((1, 3, 67), dtype=torch.bfloat16, device=cuda).as_strided((1, 1, 64), (67, 13, 1))
+    wide.copy_(c.q)
+    c.check(c.run(q=wide), ref)

@@ -142,6 +142,69 @@ def test_attention_sizes_and_a_short_workspace(kvc):
     assert kvc._lib_attention_result(FAKE + 64, None) == kvc.KVC_ERR_INVALID
 
 
+def split_model(lens, rows, heads, ratio, tile_rows, unit, target, least):
+    """The attention's split in Python: the parts (sequence, head, row tile,
+    first tile, last tile, whole, slot) of every workgroup."""
+    tiles = [-(-r * ratio // tile_rows) for r in rows]
+    real = [-(-n // unit) for n in lens]
+    total = sum(t * heads * u for t, u in zip(tiles, real))
+    per = max(-(-total // target), least)
+    aligned, tried = False, per
+    for _ in range(2):
+        if sum(t * heads * -(-u // tried) for t, u in zip(tiles, real)) <= target:
+            aligned, per = True, tried
+            break
+        tried += (tried + 7) // 8
+    items, base = [], 0
+    for b, (t, u) in enumerate(zip(tiles, real)):
+        size = -(-u // per) * per if aligned else u
+        for i in range(t * heads):
+            items.append((base, size, u, b, i // t, i % t))
+            base += size
+    parts = []
+    for w in range(target):
+        lo, hi = w * per, (w + 1) * per
+        for first, size, u, b, h, tile in items:
+            if first < hi and first + size > lo and size:
+                at, to = max(first, lo), min(first + size, hi)
+                parts.append((w, b, h, tile, min(at - first, u), min(to - first, u),
+                              first >= lo and first + size <= hi, 2 * w + (first >= lo), u))
+    return per, aligned, items, parts
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_the_attention_split_covers_every_token_once(seed):
+    """Every tile of every item is in exactly one part; a workgroup leaves at
+    most one part in each of its two places; the join finds an item's parts in
+    the places it reads; no place lies outside the workspace."""
+    rng = np.random.default_rng(seed)
+    batch, heads, ratio = int(rng.integers(1, 60)), int(rng.choice([1, 2, 3, 8])), int(rng.choice([1, 4, 5]))
+    wide = bool(rng.integers(2))
+    tile_rows, unit, least = (128, 64, 1) if wide else (16, 32, 4)
+    rows = rng.integers(0, 200 if wide else 5, batch)
+    lens = rng.integers(0, int(rng.choice([50, 3000, 40000])), batch) + rows
+    target = int(rng.choice([256, 512, 768]))
+    per, aligned, items, parts = split_model(lens.tolist(), rows.tolist(), heads, ratio, tile_rows, unit, target, least)
+    covered, places = {}, set()
+    for w, b, h, tile, lo, hi, whole, slot, u in parts:
+        covered.setdefault((b, h, tile), []).append((lo, hi, whole, slot))
+        if not whole:
+            assert slot not in places and slot < 2 * target
+            places.add(slot)
+    assert len(covered) == len([i for i in items if i[1]])
+    for first, size, u, b, h, tile in items:
+        if not size:
+            continue
+        got = sorted(covered[(b, h, tile)], key=lambda p: p[:2])
+        assert got[0][0] == 0 and got[-1][1] == u and all(x[1] == y[0] for x, y in zip(got, got[1:]))
+        w0, w1 = first // per, (first + size - 1) // per
+        assert w1 < target
+        if w0 == w1:
+            assert len(got) == 1 and got[0][2]
+        else:
+            assert [p[3] for p in sorted(got, key=lambda p: p[3] // 2)] == [2 * w0 + 1] + [2 * w for w in range(w0 + 1, w1 + 1)]
+
+
 def test_the_plain_block_table_conserves_pages():
     """The tests' reference itself: no page is lost or held twice, and
     trimming what a step took restores the stack."""
