@@ -75,42 +75,61 @@ __device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
         items0 = Plan::tiles(a, s) * a.heads;
         real0 = Plan::real(a, s);
     }
-    auto sum = [&](auto of_item) {              // over all items, of what their units give
-        uint32_t x = items0 * of_item(real0);
+    auto each = [&](auto add) {                 // the items and units of this lane's sequences
+        add(items0, real0);
         for (uint32_t b = 64 + lane; b < a.batch; b += 64) {
             const Seq s = seq_of(a, b);
-            x += Plan::tiles(a, s) * a.heads * of_item(Plan::real(a, s));
+            add(Plan::tiles(a, s) * a.heads, Plan::real(a, s));
         }
-        return of_lane(scan(x), 63);
     };
-    const uint32_t units = sum([](uint32_t real) { return real; });
+    uint32_t units = 0, all = 0;
+    each([&](uint32_t items, uint32_t real) {
+        units += items * real;
+        all += items;
+    });
+    units = of_lane(scan(units), 63);
     uint32_t per = (units + a.target - 1) / a.target;
     if (per < least) per = least;
     p.per = per;
+    if (of_lane(scan(all), 63) > a.target) return p;
     for (int i = 0; i < 2 && !p.aligned; ++i, per += (per + 7) / 8) {
-        if (sum([&](uint32_t real) { return (real + per - 1) / per; }) > a.target) continue;
+        uint32_t groups = 0;
+        each([&](uint32_t items, uint32_t real) { groups += items * ((real + per - 1) / per); });
+        if (of_lane(scan(groups), 63) > a.target) continue;
         p.aligned = true;
         p.per = per;
     }
     return p;
 }
 
-// The item that holds unit `at`, and where it lies.
+// The item that holds a unit, and where it lies.
 struct Share {
-    bool any;
+    bool any = false;
     Seq seq;
     uint32_t b, head, tile;
     uint32_t units, real;                       // rounded up to what workgroups take, and not
     uint32_t first;                             // its first unit
+    uint32_t tiles, begin, past;                // its sequence's: row tiles, first unit, the unit behind the last
+    uint32_t b0 = 0, base = 0;                  // the 64 sequences that the sequence is among, the units before them
 };
 
-// note: workgroup 0 writes the spans that the join reads, and the flags.
-__device__ inline Share share_of(const AttendArgs& a, const Plan& p, uint32_t at, bool note) {
+__device__ inline void item_of(Share* r, uint32_t at) {
+    const uint32_t item = (at - r->begin) / r->units;
+    r->head = __builtin_amdgcn_readfirstlane(item / r->tiles);
+    r->tile = __builtin_amdgcn_readfirstlane(item - r->head * r->tiles);
+    r->first = __builtin_amdgcn_readfirstlane(r->begin + item * r->units);
+}
+
+// Finds the item that holds unit `at`, not before what *r holds: it is looked
+// for from there on.  note: workgroup 0 writes the spans that the join reads,
+// and the flags.
+__device__ inline void share_of(const AttendArgs& a, const Plan& p, uint32_t at, Share* r, bool note) {
+    if (r->any && at < r->past) return item_of(r, at);
     const uint32_t lane = threadIdx.x & 63;
-    Share r{};
-    uint32_t base = 0;
+    uint32_t base = r->base;
     bool bad = false;
-    for (uint32_t b0 = 0; b0 < a.batch; b0 += 64) {
+    r->any = false;
+    for (uint32_t b0 = r->b0; b0 < a.batch; b0 += 64) {
         const uint32_t b = b0 + lane;
         uint32_t tiles = 0, real = 0;
         Seq s{};
@@ -127,18 +146,19 @@ __device__ inline Share share_of(const AttendArgs& a, const Plan& p, uint32_t at
         const uint64_t who = __ballot(count && at >= end - count && at < end);
         if (who) {
             const int l = __builtin_ctzll(who);
-            r.any = true;
-            r.b = b0 + l;
-            r.seq.start = static_cast<int32_t>(of_lane(s.start, l));
-            r.seq.rows = static_cast<int32_t>(of_lane(s.rows, l));
-            r.seq.context = static_cast<int32_t>(of_lane(s.context, l));
-            r.units = of_lane(u, l);
-            r.real = of_lane(real, l);
-            const uint32_t t = of_lane(tiles, l), from = of_lane(end - count, l);
-            const uint32_t item = (at - from) / r.units;
-            r.head = item / t;
-            r.tile = item - r.head * t;
-            r.first = from + item * r.units;
+            r->any = true;
+            r->b = b0 + l;
+            r->b0 = b0;
+            r->base = base;
+            r->seq.start = static_cast<int32_t>(of_lane(s.start, l));
+            r->seq.rows = static_cast<int32_t>(of_lane(s.rows, l));
+            r->seq.context = static_cast<int32_t>(of_lane(s.context, l));
+            r->units = of_lane(u, l);
+            r->real = of_lane(real, l);
+            r->tiles = of_lane(tiles, l);
+            r->begin = of_lane(end - count, l);
+            r->past = of_lane(end, l);
+            item_of(r, at);
             if (!note) break;
         }
         base = of_lane(end, 63);
@@ -155,10 +175,6 @@ __device__ inline Share share_of(const AttendArgs& a, const Plan& p, uint32_t at
             a.ctl->aligned = p.aligned;
         }
     }
-    r.head = __builtin_amdgcn_readfirstlane(r.head);
-    r.tile = __builtin_amdgcn_readfirstlane(r.tile);
-    r.first = __builtin_amdgcn_readfirstlane(r.first);
-    return r;
 }
 
 // Workgroups are dealt to the eight XCDs in turn; this numbers them so that

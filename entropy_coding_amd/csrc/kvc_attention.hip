@@ -71,8 +71,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
     const uint32_t from = place * plan.per, end = from + plan.per;
     uint32_t at = from;
     bool note = blockIdx.x == 0 && wave == 0;
+    Share sh;
     while (at < end) {
-        const Share sh = share_of(a, plan, at, note);
+        share_of(a, plan, at, &sh, note);
         note = false;
         if (!sh.any) break;
         const Part pt = part_of(a, sh, place, at, from, end, kTile);
@@ -472,7 +473,11 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     s.wide = usual > 16;
     s.row_tiles = !s.wide || usual <= 64 || channels > 192 ? 1 : 2;
     s.tile_shift = !s.wide ? 4 : s.row_tiles == 1 ? 6 : s.row_tiles == 2 ? 7 : 8;
-    s.split = max_tokens > (s.wide ? 512 : 1024);
+    // Long sequences are split.  Of short ones each item gets a workgroup and no join is launched (one token over 512
+    // tokens: 10.2 us instead of 12.4; 200 sequences of up to 500: 61 instead of 108); but each reads the lengths up to
+    // its own, so that many sequences are dealt to fewer workgroups, which go on where they are (1000 sequences of up
+    // to 300 tokens: 279 us and dealt 247, with six drafted tokens each 338 and 421; 4000 of up to 100: 2117 and 521).
+    s.split = max_tokens > (s.wide ? 512 : 1024) || batch > 1024;
     // every sequence's rows fill whole tiles but the last one
     const uint64_t tile_rows = uint64_t(1) << s.tile_shift;
     const uint64_t items = uint64_t(heads) * (uint64_t(rows) * ratio / tile_rows + (rows < batch ? rows : batch));

@@ -67,7 +67,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     uint32_t at = from;
     bool note = blockIdx.x == 0 && wave == 0;
     while (at < end) {
-        const Share sh = share_of(a, plan, at, note);
+        Share sh;
+        share_of(a, plan, at, &sh, note);
         note = false;
         if (!sh.any) break;
         const Part pt = part_of(a, sh, place, at, from, end, kWideTile);

@@ -44,16 +44,21 @@ bool read_back(void* h, const void* d, uint64_t bytes, hipStream_t s) {
 
 // ---- attention
 
+// The scale of the scores in units of log 2.
+float score_scale(const kvc_attention* p) {
+    return static_cast<float>(double(p->softmax_scale) * double(p->k_scale) * 1.4426950408889634);
+}
+
 // The sizes of a call (all that kvc_paged_attention_sizes looks at).
 bool attention_sizes_ok(const kvc_paged_kv* g, const kvc_attention* p) {
     if (!p || !pools_ok(g, 0, p->kv_dtype, p->channels)) return false;
-    if (p->channels > 256 || g->batch < 1 || g->batch > 1 << 20 || g->max_pages < 1 || g->max_pages >= kInt31 || g->batch * g->max_pages > kMaxScalars)
-        return false;
+    // (every workgroup reads all lengths: a batch has a bound)
+    if (p->channels > 256 || g->batch < 1 || g->batch > 1 << 14 || g->max_pages < 1 || g->max_pages >= kInt31) return false;
     if (uint64_t(g->num_pages) * g->page_tokens >= uint64_t(kInt31)) return false;
     if (p->rows < 0 || p->rows >= 1 << 24 || p->rows_per_sequence < 0 || p->max_tokens < 0) return false;
     if (p->q_heads < 1 || p->q_heads % g->heads || p->q_heads / g->heads > 1024) return false;
     if (p->rows * p->q_heads >= kInt31) return false;
-    return std::isfinite(p->softmax_scale) && positive(p->k_scale) && positive(p->v_scale);
+    return std::isfinite(score_scale(p)) && positive(p->k_scale) && positive(p->v_scale);
 }
 
 bool attention_ok(const kvc_paged_kv* g, const kvc_attention* p) {
@@ -200,7 +205,7 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
     a.mask = p->d_tree_mask;
     a.mask_words = static_cast<uint32_t>(p->mask_words);
     a.rows = static_cast<uint32_t>(p->rows);
-    a.scale_log2 = static_cast<float>(double(p->softmax_scale) * double(p->k_scale) * 1.4426950408889634);
+    a.scale_log2 = score_scale(p);
     a.v_scale = p->v_scale;
     a.target = shape.grid;
     a.split = shape.split;

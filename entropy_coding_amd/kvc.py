@@ -674,6 +674,8 @@ class PagedAttention:
             _tensor(context_lens, "context_lens", torch.int32, (self.batch,), dev)
         if tree_mask is not None:
             _tensor(tree_mask, "tree_mask", torch.int64, (rows, None), dev)
+            if tree_mask.shape[1] == 0:
+                raise ValueError("tree_mask needs a word a row")
         if out is None or lse is None:
             with torch.cuda.stream(stream):
                 out = torch.empty((rows, self.q_heads, ch), dtype=q.dtype, device=dev) if out is None else out
@@ -684,7 +686,7 @@ class PagedAttention:
         d.d_q, d.q_row_stride, d.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
         d.d_out, d.out_row_stride, d.d_lse = out.data_ptr(), out.stride(0), lse.data_ptr()
         d.d_row_starts, d.d_context_lens = row_starts.data_ptr(), _ptr(context_lens)
-        d.d_tree_mask, d.mask_words = _ptr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1]
+        d.d_tree_mask, d.mask_words = _ptr(tree_mask), tree_mask.shape[1] if tree_mask is not None and rows else 0
         d.rows = rows
         ws, paged = self.workspace, self.paged
         st = _queue(dev, stream,

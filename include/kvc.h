@@ -448,8 +448,8 @@ int kvc_block_table_result(const void* d_workspace, void* stream, int64_t* h_row
  * layer + 1, a slot being page x page_tokens + row as kvc_build_block_table
  * gives it.  Rows whose slot is negative or past the pool are skipped; two
  * rows of one slot leave a mix of both.  kv_dtype is the pools' type:
- * values of the same type are copied bit for bit; bf16 into e4m3 is
- * x / k_scale (x / v_scale) rounded to nearest even, what lies beyond +-448
+ * values of the same type are copied bit for bit; bf16 into e4m3 is the
+ * float32 quotient x / k_scale (x / v_scale) rounded to nearest even, what lies beyond +-448
  * saturated, NaN kept.  Scales are finite and positive, and 1 when the types
  * are the same.  h_paged as for kvc_decode_paged (its table is not read and
  * may be NULL).  d_k and d_v 16-byte aligned, row strides (in values, at
@@ -480,8 +480,9 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * to bf16 for the matrix instructions, the output to bf16.  Rows behind
  * d_row_starts[batch] are left as they were.
  * q and out bf16, the cache bf16 or e4m3; channels 64, 128, 192 or 256;
- * q_heads a multiple of heads, at most 1024 per KV head.  num_pages x
- * page_tokens < 2^31.
+ * q_heads a multiple of heads, at most 1024 per KV head, rows x q_heads <
+ * 2^31; at most 16384 sequences; num_pages x page_tokens < 2^31;
+ * softmax_scale x k_scale / log 2 a finite float32.
  * rows_per_sequence and max_tokens shape the launch only; results do not
  * depend on them: the usual n_b (0: rows / batch) and the longest context +
  * n_b (0: max_pages x page_tokens).

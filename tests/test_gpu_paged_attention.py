@@ -386,3 +386,65 @@ def test_one_row_or_one_head_of_any_stride(kvc, cuda):
     wide = torch.zeros((1, 3, 67), dtype=torch.bfloat16, device=cuda).as_strided((1, 1, 64), (67, 13, 1))
     wide.copy_(c.q)
     c.check(c.run(q=wide), ref)
+
+
+def test_masks_without_rows_or_words(kvc, cuda):
+    c = Case(kvc, cuda, [20, 3], [2, 1], 1, 1, 64, "bf16", 16, False, seed=25)
+    att = kvc.PagedAttention(c.paged(), 1, 3)
+    starts, contexts = c.dev(c.starts), c.dev(c.contexts)
+    with pytest.raises(ValueError):                        # no words: not the same as no mask
+        att(1, c.q, starts, contexts, torch.zeros((3, 0), dtype=torch.int64, device=cuda))
+    att(1, c.q[:0], torch.zeros_like(starts), contexts, torch.zeros((0, 1), dtype=torch.int64, device=cuda))
+    att.result()
+
+
+@pytest.mark.parametrize("nodes", [1, 9])
+def test_large_batches(kvc, cuda, nodes):
+    """More items than workgroups, sequences far behind the first 64, empty
+    ones between them; split or an item a workgroup."""
+    rng = np.random.default_rng(26)
+    batch = 1500
+    contexts, rows = rng.integers(0, 40, batch), rng.integers(0, nodes + 1, batch)
+    contexts[[0, 700, 1499]], rows[[0, 700, 1499]] = 2000, nodes
+    c = Case(kvc, cuda, contexts, rows, 2, 2, 64, "bf16", 16, False, seed=27)
+    ref = c.ref()
+    for hint in (nodes, 30):
+        c.check(c.run(hint=hint), ref)
+        c.check(c.run(hint=hint, most=60), ref)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [[3, 2], [70, 40]])
+def test_wild_values_of_split_sequences(kvc, cuda, kind, nodes):
+    """NaN (and infinities of bf16) in V of drafted tokens where several
+    workgroups share a sequence."""
+    c = Case(kvc, cuda, [3000, 500], nodes, 2, 4, 128, kind, 16, True, seed=28)
+    v = c.pools[2 * c.layer + 1].view(-1, 2, 128)
+    for b, j, ch, x in ((0, 1, 5, float("nan")), (0, nodes[0] - 1, 127, float("inf")), (1, 0, 64, float("-inf"))):
+        t = int(c.contexts[b]) + j
+        v[int(c.table[b, t // 16]) * 16 + t % 16, :, ch] = x
+    ref = c.ref()
+    got = c.run()
+    o, out = R.to_f64(got[0]), np.array(ref[0])
+    # an unseen one has weight 0 in the plain form, which leaves it out by rows
+    special = ~np.isfinite(out)
+    assert special.any() and np.array_equal(np.isnan(o), np.isnan(out))
+    assert np.array_equal(o[np.isinf(out)], out[np.isinf(out)])
+    tol_out, tol_lse = R.tolerances(np.where(special, 0.0, out), np.where(special, 0.0, ref[2]), ref[3], 3100, 128)
+    assert (np.abs(o - out)[~special] <= tol_out[~special]).all()
+    assert (np.abs(R.to_f64(got[1]) - ref[1]) <= tol_lse).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 12, 7])
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+def test_every_kernel(kvc, cuda, d, page, kind):
+    """Each channel count, type and way of finding pages, with few rows, up to
+    64 and more a KV head, short and split, trees and chains, over tiles that
+    masks cut."""
+    for tree in (True, False):
+        c = Case(kvc, cuda, [90, 1100, 5], [70, 33, 40], 1, 2, d, kind, page, tree, seed=29)
+        ref = c.ref()
+        for hint in (1, 20, 70):
+            for most in (0, 100):
+                c.check(c.run(hint=hint, most=most), ref)

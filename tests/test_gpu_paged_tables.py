@@ -87,6 +87,44 @@ def test_steps_of_a_batch(kvc, cuda, batch, page, longest, new, max_rows, apart)
     s.step(None, np.zeros(batch, np.int64), False)
 
 
+@pytest.mark.parametrize("batch,max_rows", [(40, 200), (40, 3000), (1100, 9000)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_requests_that_come_with_tokens_and_no_pages(kvc, cuda, batch, max_rows, fresh):
+    """A cache that was decoded elsewhere, or a prefix to be filled: pages for
+    the cached tokens are taken along with those of the new ones, whole pages,
+    page borders and single tokens among them."""
+    rng = np.random.default_rng(batch + fresh)
+    cached = rng.integers(0, 200, batch)
+    cached[:8] = [0, 1, 15, 16, 17, 32, 160, 199]
+    held = np.minimum(rng.integers(0, 3, batch) * rng.integers(0, 2, batch), -(-cached // 16))
+    new = rng.integers(0, 6, batch) if fresh else np.zeros(batch, np.int64)
+    if fresh:
+        new[:8] = [0, 15, 1, 0, 15, 16, 2, 40]
+    s = State(kvc, cuda, batch, 16, 16, 16 * batch, held, max_rows, 9)
+    s.step(cached, new if fresh else None, False)
+    s.step(cached, None, True)
+
+
+@pytest.mark.parametrize("batch", [5, 1100])
+def test_without_slots_or_positions(kvc, cuda, batch):
+    """The maps are left out singly or both: the table and the row starts are
+    the same, and without them no number of rows is too large."""
+    i32 = dict(dtype=torch.int32, device=cuda)
+    got = []
+    for slots, positions in ((True, True), (True, False), (False, True), (False, False)):
+        t = kvc.BlockTable(torch.full((batch, 8), -1, **i32), torch.zeros(batch, **i32),
+                           torch.arange(8 * batch, **i32), torch.full((1,), 8 * batch, **i32), 16, 8 * batch,
+                           torch.zeros(batch + 1, **i32),
+                           torch.zeros(128 * batch, dtype=torch.int64, device=cuda) if slots else None,
+                           torch.zeros(128 * batch, **i32) if positions else None)
+        new = torch.arange(batch, **i32) % 129
+        t(None, new)
+        assert t.result() == int(new.sum())
+        got.append((t.block_table, t.row_starts, t.held, t.free_count))
+    for g in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], g))
+
+
 def test_trim_undoes_a_step(kvc, cuda):
     s = State(kvc, cuda, 5, 16, 10, 64, [1, 0, 2, 3, 1], 200, 3)
     before, count = s.free.copy(), s.count

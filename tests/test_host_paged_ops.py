@@ -105,7 +105,8 @@ SIZES_BAD = [
     dict(q_heads=8 * 1025), dict(softmax_scale=math.nan), dict(softmax_scale=math.inf), dict(k_scale=0.0),
     dict(v_scale=-2.0), dict(batch=0), dict(batch=(1 << 20) + 1), dict(max_pages=0), dict(heads=0),
     dict(page_tokens=0), dict(num_pages=11), dict(num_pages=1 << 28, pool_bytes=1 << 62), dict(reserved=3),
-    dict(n_pools=1), dict(d_pools=None),
+    dict(n_pools=1), dict(d_pools=None), dict(batch=(1 << 14) + 1), dict(softmax_scale=3e38),
+    dict(softmax_scale=1e30, k_scale=1e30),
 ]
 
 
