@@ -13,6 +13,18 @@
 // waves 2 and 3 of V.  Two tiles fit: the next one is on its way from memory to
 // registers while the current one is multiplied, and is written beside it
 // before the one barrier of a tile.
+//
+// What bounds it: with 128 channels and RT = 2 a wave's tile takes 64 matrix
+// instructions of 16 cycles and about as many cycles of vector instructions
+// (32 exponentials at 16 cycles, 150 others at 4), and the two waves that a
+// SIMD holds overlap them in part.  Two pieces of 1000 tokens behind 7001
+// cached ones (8 KV heads, 4 query heads each, bf16: 246 GFLOP) take 270 to
+// 282 us, 870 to 910 TFLOP/s, where a library's large matrix product reaches 1390 on the same
+// card; matrix units busy 32% of the time, vector units 35%, LDS 25% without
+// conflicts.  RT = 4 needs registers that a wave does not have, and 64 rows
+// (RT = 1) read each operand from LDS for half as many products.  Tried and
+// slower: the tile after the next on its way too (4 sequences of 16 drafted
+// tokens over 4096: 30.2 us instead of 28.3).
 #include "kvc_attend_device.hpp"
 
 #include <type_traits>
@@ -194,22 +206,24 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
         auto compute = [&](int t, int buf, auto held) {
             constexpr int G = held;             // groups that have rows
             const int t0 = t * kWideTile;
+            // (the waves that multiply go before those that form weights on the same SIMD: 3%)
             __builtin_amdgcn_s_setprio(1);
             // Operands are read from LDS kAhead before their products: one by one, each pair of products would wait for
-            // a whole trip to LDS.
+            // a whole trip to LDS (the pieces of a prompt above 369 us and, so, 315 at the time).  The four sums of a group take
+            // turns, so that no product waits for the one before it (0.7%).
             u32x4 ring[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) ring[i] = lds.k[buf][i][lane];
+            for (int i = 0; i < kAhead; ++i) ring[i] = lds.k[buf][(i & 3) * KK + (i >> 2)][lane];
             __builtin_amdgcn_sched_barrier(0);
             f32x4 s[G][4];
 #pragma unroll
             for (int i = 0; i < 4 * KK; ++i) {
-                const int hf = i / KK, kk = i % KK;
+                const int hf = i & 3, kk = i >> 2;
                 const bf16x8 kf = __builtin_bit_cast(bf16x8, ring[i % kAhead]);
 #pragma unroll
                 for (int rt = 0; rt < G; ++rt)
                     s[rt][hf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][kk], kk ? s[rt][hf] : f32x4{0, 0, 0, 0}, 0, 0, 0);
-                if (i + kAhead < 4 * KK) ring[i % kAhead] = lds.k[buf][i + kAhead][lane];
+                if (i + kAhead < 4 * KK) ring[i % kAhead] = lds.k[buf][((i + kAhead) & 3) * KK + ((i + kAhead) >> 2)][lane];
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (t0 + kWideTile > pt.full) {
