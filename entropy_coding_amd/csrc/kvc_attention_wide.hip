@@ -10,7 +10,7 @@
 // lane: K in 4 x D / 32 of them (16 tokens x 32 channels), V^T in 2 x D / 16
 // (16 channels x 32 tokens).  Writes and reads are 16 bytes a lane in lane
 // order, free of bank conflicts.  Waves 0 and 1 stage 32 tokens of K each,
-// waves 2 and 3 of V.  Two tiles fit: the next one is on its way from memory to
+// waves 2 and 3 of V.  As a rule two tiles fit: the next one is on its way from memory to
 // registers while the current one is multiplied, and is written beside it
 // before the one barrier of a tile.
 //
@@ -37,21 +37,33 @@ constexpr int kWideTile = 64;
 constexpr int kAhead = 4;
 constexpr int kNoDs = 0x7F;                     // the scheduler may move all across but LDS instructions
 
+// Tiles in LDS: two, and one where two would keep a second workgroup off the
+// CU that the registers have room for (e4m3, whose staged tile takes half the
+// registers, with 192 and 256 channels): the next tile is then written between
+// two barriers, while the other workgroup multiplies.  32 sequences of 16
+// drafted tokens over up to 4096: 135 us and so 78 with 192 channels, 114 and
+// 84 with 256 (4 sequences: 39 and 34, 37 and 40).  In bf16, whose registers
+// are short then, 192 channels gain with 32 sequences (124 and 103 us) and lose
+// with one of 32000 tokens (56 and 62); a third workgroup for e4m3 of 128
+// channels likewise (57 and 49; 4 sequences: 26 and 29).
+constexpr int bufs_of(int d, bool fp8, int rt) { return rt == 1 && d >= 192 && fp8 ? 1 : 2; }
+
 // Workgroups (of a wave a SIMD) that a CU can hold at once: by the registers
 // of a wave (sums, queries, scores, weights, the staged quarter of a tile and
-// about 80 for the rest, of 512) and by two tiles of 160 KB of LDS.
+// about 80 for the rest, of 512) and by the tiles in 160 KB of LDS.
 constexpr int groups_of(int d, bool fp8, int rt) {
     const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 80;
     const int regs = need <= 168 ? 3 : need <= 256 ? 2 : 1;
-    const int fit = 160 * 1024 / (2 * kWideTile * d * 4 + 256);
+    const int fit = 160 * 1024 / (bufs_of(d, fp8, rt) * kWideTile * d * 4 + 256);
     return regs < fit ? regs : fit;
 }
 
-template <int D>
+template <int D, int BUFS>
 struct WideLds {
-    u32x4 k[2][4 * (D / 32)][64];
-    u32x4 v[2][2 * (D / 16)][64];
+    u32x4 k[BUFS][4 * (D / 32)][64];
+    u32x4 v[BUFS][2 * (D / 16)][64];
 };
+
 
 // PAGE: 16, 4 or 1, the largest that divides the tokens of a page: with 16 a
 // half of a wave's 32 tokens lies in one page, its rows a constant stride
@@ -65,7 +77,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     constexpr int KK = D / 32;                  // products over the channels
     constexpr int N4 = 2 * KG;                  // 16-byte registers a lane stages, of K or of V
     constexpr int VS = PAGE == 1 ? 8 : 2;
-    __shared__ WideLds<D> lds;
+    constexpr int kBufs = bufs_of(D, FP8, RT);
+    __shared__ WideLds<D, kBufs> lds;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -290,14 +303,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             write(ta, 0);
             __syncthreads();
             for (int t = ta; t < tb; ++t) {
-                const int buf = (t - ta) & 1;
+                const int buf = kBufs == 2 ? (t - ta) & 1 : 0;
                 if (t + 1 < tb) {
                     load(t + 1);
                     read_pages(t + 2);
                 }
                 if (RT == 2 && groups > 1) compute(t, buf, std::integral_constant<int, RT>{});
                 else if (groups) compute(t, buf, std::integral_constant<int, 1>{});
-                if (t + 1 < tb) write(t + 1, buf ^ 1);
+                if (kBufs == 1) __syncthreads();
+                if (t + 1 < tb) write(t + 1, kBufs == 2 ? buf ^ 1 : 0);
                 __syncthreads();
             }
         }
