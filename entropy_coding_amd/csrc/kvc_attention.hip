@@ -481,8 +481,16 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     AttendShape s;
     const int64_t usual = (rows_per_sequence > 0 ? rows_per_sequence : (rows + batch - 1) / batch) * ratio;
     s.wide = usual > 16;
-    s.row_tiles = !s.wide || usual <= 64 || channels > 192 ? 1 : 2;
-    s.tile_shift = !s.wide ? 4 : s.row_tiles == 1 ? 6 : s.row_tiles == 2 ? 7 : 8;
+    // Two groups of 16 rows a wave halve the reads of LDS for a product.  Beyond 128 channels their sums leave room for
+    // one workgroup a CU, and two workgroups of one group a wave are faster, where LDS holds one tile each instead of
+    // two (two pieces of 1000 tokens over 7001 with 192 channels: bf16 997 and 767 us, e4m3 781 and 620; with 256 and one
+    // workgroup 1287, two 839).  In bf16 that second workgroup is paid for with registers, so that up to 64 rows, which
+    // wait for K and V, keep one (two sequences of 32000 tokens, 192 channels: 56 and 62 us, 256: 67 and 80; but 32 of up
+    // to 4096, 192 channels: 124 and 103); e4m3 gains there as well (67 and 49; 52 and 53; 135 and 78).  A third
+    // workgroup by the same means, e4m3 of 128 channels: 57 and 49 us, but with 4 sequences 26 and 29.
+    s.row_tiles = !s.wide || usual <= 64 || channels > 128 ? 1 : 2;
+    s.lds_tiles = channels > 128 && (fp8 || usual > 64) ? 1 : 2;
+    s.tile_shift = !s.wide ? 4 : s.row_tiles == 1 ? 6 : 7;
     // Long sequences are split.  Of short ones each item gets a workgroup and no join is launched (one token over 512
     // tokens: 10.2 us instead of 12.4; 200 sequences of up to 500: 61 instead of 108); but each reads the lengths up to
     // its own, so that many sequences are dealt to fewer workgroups, which go on where they are (1000 sequences of up
@@ -494,7 +502,7 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     s.unit_shift = s.wide ? 6 : 5;
     while (items * ((uint64_t(widest) >> s.unit_shift) + 1) >= (uint64_t(1) << 30)) ++s.unit_shift;
     uint64_t grid = items;
-    if (s.split) grid = 256u * (s.wide ? wide_groups(channels, fp8, s.row_tiles) : waves_of(static_cast<int>(channels), fp8));
+    if (s.split) grid = 256u * (s.wide ? wide_groups(channels, fp8, s.row_tiles, s.lds_tiles) : waves_of(static_cast<int>(channels), fp8));
     if (grid < 1) grid = 1;
     s.grid = static_cast<uint32_t>(grid);
     const auto up = [](uint64_t x) { return (x + 255) / 256 * 256; };

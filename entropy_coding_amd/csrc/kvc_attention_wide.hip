@@ -10,18 +10,18 @@
 // lane: K in 4 x D / 32 of them (16 tokens x 32 channels), V^T in 2 x D / 16
 // (16 channels x 32 tokens).  Writes and reads are 16 bytes a lane in lane
 // order, free of bank conflicts.  Waves 0 and 1 stage 32 tokens of K each,
-// waves 2 and 3 of V.  As a rule two tiles fit: the next one is on its way from memory to
-// registers while the current one is multiplied, and is written beside it
-// before the one barrier of a tile.
+// waves 2 and 3 of V.  The next tile is on its way from memory to registers
+// while the current one is multiplied; it is then written beside it before
+// the one barrier of a tile or, where LDS holds one tile only, between two.
 //
 // What bounds it: with 128 channels and RT = 2 a wave's tile takes 64 matrix
 // instructions of 16 cycles and about as many cycles of vector instructions
 // (32 exponentials at 16 cycles, 150 others at 4), and the two waves that a
 // SIMD holds overlap them in part.  Two pieces of 1000 tokens behind 7001
 // cached ones (8 KV heads, 4 query heads each, bf16: 246 GFLOP) take 270 to
-// 282 us, 870 to 910 TFLOP/s, where a library's large matrix product reaches 1390 on the same
-// card; matrix units busy 32% of the time, vector units 35%, LDS 25% without
-// conflicts.  RT = 4 needs registers that a wave does not have, and 64 rows
+// 282 us, 870 to 910 TFLOP/s, where a library's large matrix product reaches
+// 1390 on the same card; matrix units busy 32% of the time, vector units 35%,
+// LDS 25% without conflicts.  RT = 4 needs registers that a wave does not have, and 64 rows
 // (RT = 1) read each operand from LDS for half as many products.  Tried and
 // slower: the tile after the next on its way too (4 sequences of 16 drafted
 // tokens over 4096: 30.2 us instead of 28.3).
@@ -37,24 +37,13 @@ constexpr int kWideTile = 64;
 constexpr int kAhead = 4;
 constexpr int kNoDs = 0x7F;                     // the scheduler may move all across but LDS instructions
 
-// Tiles in LDS: two, and one where two would keep a second workgroup off the
-// CU that the registers have room for (e4m3, whose staged tile takes half the
-// registers, with 192 and 256 channels): the next tile is then written between
-// two barriers, while the other workgroup multiplies.  32 sequences of 16
-// drafted tokens over up to 4096: 135 us and so 78 with 192 channels, 114 and
-// 84 with 256 (4 sequences: 39 and 34, 37 and 40).  In bf16, whose registers
-// are short then, 192 channels gain with 32 sequences (124 and 103 us) and lose
-// with one of 32000 tokens (56 and 62); a third workgroup for e4m3 of 128
-// channels likewise (57 and 49; 4 sequences: 26 and 29).
-constexpr int bufs_of(int d, bool fp8, int rt) { return rt == 1 && d >= 192 && fp8 ? 1 : 2; }
-
 // Workgroups (of a wave a SIMD) that a CU can hold at once: by the registers
 // of a wave (sums, queries, scores, weights, the staged quarter of a tile and
 // about 80 for the rest, of 512) and by the tiles in 160 KB of LDS.
-constexpr int groups_of(int d, bool fp8, int rt) {
+constexpr int groups_of(int d, bool fp8, int rt, int bufs) {
     const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 80;
-    const int regs = need <= 168 ? 3 : need <= 256 ? 2 : 1;
-    const int fit = 160 * 1024 / (bufs_of(d, fp8, rt) * kWideTile * d * 4 + 256);
+    const int regs = need <= 168 ? 3 : need <= 264 ? 2 : 1;
+    const int fit = 160 * 1024 / (bufs * kWideTile * d * 4 + 256);
     return regs < fit ? regs : fit;
 }
 
@@ -64,12 +53,12 @@ struct WideLds {
     u32x4 v[BUFS][2 * (D / 16)][64];
 };
 
-
 // PAGE: 16, 4 or 1, the largest that divides the tokens of a page: with 16 a
 // half of a wave's 32 tokens lies in one page, its rows a constant stride
 // apart; with 4 a lane's run of four V rows does.
-template <int D, bool FP8, int RT, int PAGE>
-__global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_wide(AttendArgs a) {
+// BUFS: tiles that LDS holds.
+template <int D, bool FP8, int RT, int BUFS, int PAGE>
+__global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_attend_wide(AttendArgs a) {
     constexpr int C = D / 16;                   // channels of V a lane stages
     constexpr int ES = FP8 ? 1 : 2;
     constexpr int VW = C * ES / 4;              // words of them
@@ -77,8 +66,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     constexpr int KK = D / 32;                  // products over the channels
     constexpr int N4 = 2 * KG;                  // 16-byte registers a lane stages, of K or of V
     constexpr int VS = PAGE == 1 ? 8 : 2;
-    constexpr int kBufs = bufs_of(D, FP8, RT);
-    __shared__ WideLds<D, kBufs> lds;
+    __shared__ WideLds<D, BUFS> lds;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -303,15 +291,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
             write(ta, 0);
             __syncthreads();
             for (int t = ta; t < tb; ++t) {
-                const int buf = kBufs == 2 ? (t - ta) & 1 : 0;
+                const int buf = BUFS == 2 ? (t - ta) & 1 : 0;
                 if (t + 1 < tb) {
                     load(t + 1);
                     read_pages(t + 2);
                 }
                 if (RT == 2 && groups > 1) compute(t, buf, std::integral_constant<int, RT>{});
                 else if (groups) compute(t, buf, std::integral_constant<int, 1>{});
-                if (kBufs == 1) __syncthreads();
-                if (t + 1 < tb) write(t + 1, kBufs == 2 ? buf ^ 1 : 0);
+                if (BUFS == 1) __syncthreads();
+                if (t + 1 < tb) write(t + 1, BUFS == 2 ? buf ^ 1 : 0);
                 __syncthreads();
             }
         }
@@ -385,17 +373,17 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT)) void k_attend_w
     if (threadIdx.x == 0) a.words[blockIdx.x] = any ? kPagedInvalid : 0u;
 }
 
+template <int D, bool FP8, int RT, int BUFS, int PAGE>
+hipError_t launch_one(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
+    k_attend_wide<D, FP8, RT, BUFS, PAGE><<<sh.grid, 64 * kWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int D, bool FP8, int PAGE>
 hipError_t launch(const AttendArgs& a, const AttendShape& sh, hipStream_t s) {
-    if (sh.row_tiles == 1) {
-        k_attend_wide<D, FP8, 1, PAGE><<<sh.grid, 64 * kWaves, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    if constexpr (D <= 192) {
-        k_attend_wide<D, FP8, 2, PAGE><<<sh.grid, 64 * kWaves, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    return hipErrorInvalidValue;
+    if constexpr (D <= 128) return sh.row_tiles == 1 ? launch_one<D, FP8, 1, 2, PAGE>(a, sh, s) : launch_one<D, FP8, 2, 2, PAGE>(a, sh, s);
+    else if constexpr (FP8) return launch_one<D, FP8, 1, 1, PAGE>(a, sh, s);
+    else return sh.lds_tiles == 1 ? launch_one<D, FP8, 1, 1, PAGE>(a, sh, s) : launch_one<D, FP8, 1, 2, PAGE>(a, sh, s);
 }
 
 template <int D>
@@ -407,8 +395,8 @@ hipError_t launch_channels(const AttendArgs& a, const AttendShape& sh, bool fp8,
 
 }  // namespace
 
-int wide_groups(int64_t channels, bool fp8, int row_tiles) {
-    return groups_of(static_cast<int>(channels), fp8, row_tiles);
+int wide_groups(int64_t channels, bool fp8, int row_tiles, int lds_tiles) {
+    return groups_of(static_cast<int>(channels), fp8, row_tiles, lds_tiles);
 }
 
 hipError_t launch_attend_wide(const AttendArgs& a, const AttendShape& sh, int64_t channels, bool fp8, hipStream_t s) {

@@ -98,6 +98,7 @@ struct AttendSpan {                     // a sequence on the line of units
 struct AttendShape {                    // what the launch is made for
     bool wide;                          // rows over the waves (kvc_attention_wide.hip), not tokens
     int row_tiles;                      // 16-row tiles a wave holds
+    int lds_tiles;                      // tiles of tokens that LDS holds (wide)
     uint32_t tile_shift;                // 2^tile_shift rows of a workgroup
     uint32_t unit_shift;                // 2^unit_shift tokens of a unit of work
     uint32_t grid;                      // workgroups; where items may be split: that fill the chip
@@ -134,6 +135,6 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
                          int64_t rows_per_sequence, int64_t max_tokens, int64_t widest);
 hipError_t launch_attend(const AttendArgs& args, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
 hipError_t launch_attend_wide(const AttendArgs& a, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);
-int wide_groups(int64_t channels, bool fp8, int row_tiles);     // workgroups of it that a CU holds
+int wide_groups(int64_t channels, bool fp8, int row_tiles, int lds_tiles);     // workgroups of it that a CU holds
 
 }  // namespace kvc
