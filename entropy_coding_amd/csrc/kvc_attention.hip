@@ -216,11 +216,14 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
                     }
                 }
                 if (__any(wild != 0)) {
+                    // (of drafted tokens alone: every row sees those of the context)
                     any_wild = true;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < 8; ++j) {
+                        if (t0 + (j < 4 ? 0 : 12) + q4 * 4 + j < ctx) continue;
 #pragma unroll
                         for (int i = 0; i < VW; ++i) vw[j].set(i, without_wild<FP8>(vw[j][i]));
+                    }
                 }
             }
 
