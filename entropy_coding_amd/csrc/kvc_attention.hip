@@ -170,8 +170,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
 
         // A wave takes every fourth tile.  Its K registers are free once the scores are formed and its V registers
         // once they are summed, so the next tile's K is under way during the weights and the sum, and its V during
-        // the next scores and weights.  That is the loop over tiles that every row sees in full; the others (and the
-        // last one) go through a second copy of the body, which knows of masks and prefetches nothing, so that the
+        // the next scores and weights.  That is the loop over tiles of context, which every row sees in full; the others
+        // (and the last one) go through a second copy of the body, which knows of masks and prefetches nothing, so that the
         // first has no loads under a condition, which would be waited for with the count of the other path.
         bool any_wild = false;
         auto one_tile = [&](int t, auto inner) {
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
             if constexpr (inner) load_k(w, t + kWaves);
             __builtin_amdgcn_sched_barrier(0);
 
-            if (!inner && t0 + kTile > pt.full) {
+            if (!inner && t0 + kTile > ctx) {
                 const uint32_t win = static_cast<uint32_t>(window_of(a, sh.seq.start, query.node, t0 - ctx, length - ctx));
                 uint32_t wild = 0;
 #pragma unroll
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, FP8)) void k_attend(Attend
             const Where w = find(t);
             load_k(w, t);
             load_v(w, t);
-            const int last = (tb - kWaves < pt.full / kTile ? tb - kWaves : pt.full / kTile) - 1;
+            const int last = (tb - kWaves < ctx / kTile ? tb - kWaves : ctx / kTile) - 1;
             if (t <= last) {
                 int left = (last - t) / kWaves + 1;
                 do {
@@ -366,6 +366,12 @@ __device__ uint32_t sequence_of(const int32_t* starts, uint32_t batch, uint32_t 
     }
 }
 
+// x w + y; an infinity stays one where its weight is too small for a float32,
+// as the drafted tokens' do that a part had added to it.
+__device__ inline float weighted(float x, float w, float y) {
+    return __builtin_isinf(x) ? x + y : __builtin_fmaf(x, w, y);
+}
+
 // Joins the parts of split items, by the formula above: one wave a (row,
 // query head).  N parts at a time, read before their weights are known, so
 // that a row costs two trips to memory (its place, its parts), which is what
@@ -397,13 +403,13 @@ struct Joined {
             sum = __builtin_fmaf(sum, old, __shfl(l, 0));
             top = best;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= old;
+            for (int e = 0; e < E; ++e) o[e] = weighted(o[e], old, 0.0f);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (s0 + i < parts) {
                     const float w = __shfl(f, i);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(v[i][e], w, o[e]);
+                    for (int e = 0; e < E; ++e) o[e] = weighted(v[i][e], w, o[e]);
                 }
             }
         }

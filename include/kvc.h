@@ -475,7 +475,10 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  *     o = v_scale x sum_t e^(s_t) V_t / sum_t e^(s_t)  over the tokens seen,
  *     lse = log sum_t e^(s_t);
  * a row that sees nothing has o = 0 and lse = -infinity.  What K or V hold
- * (NaN, infinity) at tokens that a row does not see has no part in it.  Sums,
+ * (NaN, infinity) at tokens that a row does not see has no part in it; an
+ * infinity in V of a drafted token that it sees is one in the output, however
+ * small its weight (of a context token whose weight is 0 in float32 it may be
+ * NaN).  Sums,
  * maxima and the output's accumulation are float32; the weights are rounded
  * to bf16 for the matrix instructions, the output to bf16.  Rows behind
  * d_row_starts[batch] are left as they were.

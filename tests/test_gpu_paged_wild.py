@@ -1,5 +1,5 @@
 """Infinities and NaN in V of the tokens that a row sees: in the context
-beside drafted ones."""
+beside drafted ones, and in tokens of hardly any weight."""
 import sys
 
 import numpy as np
@@ -61,3 +61,30 @@ def test_context_values_beside_drafted_ones(kvc, cuda, d, page, kind, hint):
             plant(c, b, ctx + drafted, NAN, 0, 20)
         for most in (0, 60):
             check(c, c.run(hint=hint, most=most), clean)
+
+
+@pytest.mark.parametrize("hint", [1, 64])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("nodes", [[3, 2], [100, 70]])
+def test_drafted_values_of_hardly_any_weight(kvc, cuda, nodes, tree, kind, hint):
+    """The drafted tokens' scores lie 400 below the first tokens': their
+    weights are 0 in float32, in a tile of their own, in a part of the
+    sequence of their own and in its join.  What is infinite in them is
+    infinite in the rows that see it (and nothing else changes)."""
+    c = Case(kvc, cuda, [2048, 33], nodes, 2, 2, 128, kind, 16, tree, seed=42, scale=1.0)
+    one = torch.zeros(128, device=cuda)
+    one[5] = 1.0
+    k = c.pools[2 * c.layer]
+    for b, high in ((0, 700), (1, 32)):
+        for pos in range(int(c.contexts[b]) + nodes[b]):
+            k[int(c.table[b, pos // 16]), pos % 16] = ((10.0 if pos < high else -10.0) * one).to(k.dtype)
+    c.q = (20.0 * one + 0.01 * c.q.float()).to(torch.bfloat16)
+    clean = c.ref()
+    for b in range(2):
+        ctx = int(c.contexts[b])
+        plant(c, b, ctx, INF, 0, 9)
+        plant(c, b, ctx + nodes[b] - 1, -INF, 1, 100)
+        plant(c, b, ctx + nodes[b] // 2, NAN, 1, 64)
+    for most in (0, 60):
+        check(c, c.run(hint=hint, most=most), clean)
