@@ -490,6 +490,7 @@ class PagedKV:
                                  block_table.shape[0], heads, block_table.shape[1], n_pages, page_tokens, 0)
         self.kv_dtype = _kv_dtype(pools[0])
         self.ref = ctypes.byref(self.desc)
+        self._own = (torch._C._cuda_getCurrentRawStream(block_table.device.index), self.ptrs)
 
 
 def kvc_decode_paged(stream_bytes, mu, sigma, prefix, paged: PagedKV, workspace, stream=None,
@@ -525,22 +526,40 @@ def _rows_contiguous(t):
     return t.numel() == 0 or t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
 
 
-def _queue(device, stream, call, *tensors):
+def _queue(device, stream, call, *tensors, own=()):
     """Runs call(stream pointer) with `device` current, on `stream` (the
     device's current one if None), and keeps the tensors' memory until the
-    work queued there is done."""
+    work queued there is done; so too on a current stream that is not the one
+    that `own`, the caller's (stream pointer, hidden tensors) pairs, were made
+    on."""
     if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        for home, t in own:
+            if raw != home:
+                t.record_stream(torch.cuda.current_stream(device))
         if torch.cuda.current_device() == device.index:
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
+            return call(raw)
         with torch.cuda.device(device):
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
+            return call(raw)
     if stream.device != device:
         raise ValueError(f"the stream is of {stream.device}, the tensors of {device}")
-    for t in tensors:
+    for t in (*tensors, *(t for _, t in own)):
         if t is not None:
             t.record_stream(stream)
     with torch.cuda.device(device):
         return call(stream.cuda_stream)
+
+
+def _workspace(nbytes: int, device):
+    """A cleared workspace for calls on any stream, as an entry of _queue's
+    `own`.  Waits for the current stream: for the clearing, and for what is
+    still queued there on memory that the workspace took over.  (A capture
+    orders both itself.)"""
+    with torch.cuda.device(device):
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+        return torch.cuda.current_stream().cuda_stream, ws
 
 
 class BlockTable:
@@ -580,7 +599,8 @@ class BlockTable:
         self.held, self.free_count = held, free_count
         self.held_out = held if held_out is None else held_out
         self.free_count_out = free_count if free_count_out is None else free_count_out
-        self.workspace = torch.zeros(256 + 12 * (batch + 64), dtype=torch.uint8, device=dev)
+        self._own = _workspace(256 + 12 * (batch + 64), dev)
+        self.workspace = self._own[1]
         self.desc = kvc_block_table(
             batch, block_table.shape[1], num_pages, free_pages.numel(), max_rows, page_tokens, 0, None, None,
             _ptr(held), _ptr(self.held_out), _ptr(block_table), _ptr(free_pages), _ptr(free_count),
@@ -600,8 +620,8 @@ class BlockTable:
         ws = self.workspace
         st = _queue(self.device, stream,
                     lambda s: _lib_block_table(self._ref, ws.data_ptr(), ws.numel(), s, None),
-                    cached_lens, new_lens, ws, self.block_table, self.held, self.held_out, self.free_pages,
-                    self.free_count, self.free_count_out, self.row_starts, self.slots, self.positions)
+                    cached_lens, new_lens, self.block_table, self.held, self.held_out, self.free_pages,
+                    self.free_count, self.free_count_out, self.row_starts, self.slots, self.positions, own=(self._own,))
         _check(st, "kvc_build_block_table")
 
     def result(self, stream=None) -> int:
@@ -628,7 +648,7 @@ def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tenso
     st = _queue(dev, stream,
                 lambda s: _lib_append(paged.ref, layer, paged.kv_dtype, ch, k.data_ptr(), v.data_ptr(), _kv_dtype(k),
                                       rows, k.stride(0), v.stride(0), slots.data_ptr(), k_scale, v_scale, s),
-                k, v, slots, paged.ptrs, *(paged.pools if stream is not None else ()))
+                k, v, slots, *(paged.pools if stream is not None else ()), own=(paged._own,))
     _check(st, "kvc_paged_append")
 
 
@@ -654,7 +674,8 @@ class PagedAttention:
         self._ref = ctypes.byref(self.desc)
         n = _U64(0)
         _check(_lib_attention_sizes(paged.ref, self._ref, ctypes.byref(n)), "kvc_paged_attention_sizes")
-        self.workspace = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
+        self._own = _workspace(n.value, self.device)
+        self.workspace = self._own[1]
 
     def __call__(self, layer: int, q: torch.Tensor, row_starts: torch.Tensor, context_lens: torch.Tensor | None = None,
                  tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -691,8 +712,8 @@ class PagedAttention:
         ws, paged = self.workspace, self.paged
         st = _queue(dev, stream,
                     lambda s: _lib_attention(paged.ref, layer, self._ref, ws.data_ptr(), ws.numel(), s),
-                    q, out, lse, row_starts, context_lens, tree_mask, ws, paged.ptrs, paged.block_table,
-                    *(paged.pools if stream is not None else ()))
+                    q, out, lse, row_starts, context_lens, tree_mask, paged.block_table,
+                    *(paged.pools if stream is not None else ()), own=(self._own, paged._own))
         _check(st, "kvc_paged_attention")
         return out, lse
 
