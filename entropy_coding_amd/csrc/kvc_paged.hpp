@@ -131,6 +131,14 @@ struct AttendArgs {
     float* partial;
     float* pairs;                       // (maximum, sum) each
 };
+// At most as many items (KV heads x tiles of rows) as a call has: every
+// sequence's rows fill whole tiles but the last one.
+inline uint64_t attend_items(int64_t batch, int64_t heads, int64_t ratio, int64_t rows, int64_t tile_rows) {
+    return uint64_t(heads) * (uint64_t(rows) * ratio / tile_rows + (rows < batch ? rows : batch));
+}
+constexpr uint64_t kMaxItems = uint64_t(1) << 30;       // of tiles of 16 rows
+constexpr int64_t kMaxTokens = 0x7FFFFF00;              // of a sequence
+
 AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t channels, bool fp8, int64_t rows,
                          int64_t rows_per_sequence, int64_t max_tokens, int64_t widest);
 hipError_t launch_attend(const AttendArgs& args, const AttendShape& shape, int64_t channels, bool fp8, hipStream_t s);

@@ -58,6 +58,7 @@ bool attention_sizes_ok(const kvc_paged_kv* g, const kvc_attention* p) {
     if (p->rows < 0 || p->rows >= 1 << 24 || p->rows_per_sequence < 0 || p->max_tokens < 0) return false;
     if (p->q_heads < 1 || p->q_heads % g->heads || p->q_heads / g->heads > 1024) return false;
     if (p->rows * p->q_heads >= kInt31) return false;
+    if (kvc::attend_items(g->batch, g->heads, p->q_heads / g->heads, p->rows, 16) >= kvc::kMaxItems) return false;
     return std::isfinite(score_scale(p)) && positive(p->k_scale) && positive(p->v_scale);
 }
 
@@ -77,8 +78,14 @@ bool attention_ok(const kvc_paged_kv* g, const kvc_attention* p) {
     return p->d_tree_mask ? p->mask_words >= 1 && p->mask_words <= 1 << 20 : p->mask_words == 0;
 }
 
+// The tokens that a row of the table has room for, at most kMaxTokens.
+int64_t widest_of(const kvc_paged_kv* g) {
+    const int64_t room = g->max_pages * int64_t(g->page_tokens);
+    return room < kvc::kMaxTokens ? room : kvc::kMaxTokens;
+}
+
 kvc::AttendShape shape_of(const kvc_paged_kv* g, const kvc_attention* p) {
-    const int64_t widest = g->max_pages * int64_t(g->page_tokens);
+    const int64_t widest = widest_of(g);
     const int64_t longest = p->max_tokens > 0 && p->max_tokens < widest ? p->max_tokens : widest;
     return kvc::attend_shape(g->batch, g->heads, p->q_heads / g->heads, p->channels, p->kv_dtype == KVC_E4M3, p->rows,
                              p->rows_per_sequence, longest, widest);
@@ -186,8 +193,7 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
     a.block_table = h_paged->d_block_table;
     a.max_pages = h_paged->max_pages;
     a.num_pages = h_paged->num_pages;
-    const int64_t room = h_paged->max_pages * int64_t(h_paged->page_tokens);
-    a.max_tokens = static_cast<int32_t>(room < 0x7FFFFF00 ? room : 0x7FFFFF00);
+    a.max_tokens = static_cast<int32_t>(widest_of(h_paged));
     a.tile_shift = shape.tile_shift;
     a.unit_shift = shape.unit_shift;
     a.page_tokens = h_paged->page_tokens;

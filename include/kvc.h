@@ -484,7 +484,8 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * d_row_starts[batch] are left as they were.
  * q and out bf16, the cache bf16 or e4m3; channels 64, 128, 192 or 256;
  * q_heads a multiple of heads, at most 1024 per KV head, rows x q_heads <
- * 2^31; at most 16384 sequences; num_pages x page_tokens < 2^31;
+ * 2^31; at most 16384 sequences; heads x (rows x (q_heads / heads) / 16 +
+ * min(rows, batch)) < 2^30; num_pages x page_tokens < 2^31;
  * softmax_scale x k_scale / log 2 a finite float32.
  * rows_per_sequence and max_tokens shape the launch only; results do not
  * depend on them: the usual n_b (0: rows / batch) and the longest context +
