@@ -504,9 +504,10 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     // tokens: 10.2 us instead of 12.4; 200 sequences of up to 500: 61 instead of 108); but each reads the lengths up to
     // its own, so that many sequences are dealt to fewer workgroups, which go on where they are (1000 sequences of up
     // to 300 tokens: 279 us and dealt 247, with six drafted tokens each 338 and 421; 4000 of up to 100: 2117 and 521).
+    // (A launch has fewer than 2^32 threads.)
     const uint64_t tile_rows = uint64_t(1) << s.tile_shift;
     const uint64_t items = attend_items(batch, heads, ratio, rows, tile_rows);
-    s.split = max_tokens > (s.wide ? 512 : 1024) || batch > 1024;
+    s.split = max_tokens > (s.wide ? 512 : 1024) || batch > 1024 || items >= uint64_t(1) << 24;
     // ends at 31 at the latest: items < kMaxItems, widest <= kMaxTokens
     s.unit_shift = s.wide ? 6 : 5;
     while (items * ((uint64_t(widest) >> s.unit_shift) + 1) >= kMaxItems) ++s.unit_shift;

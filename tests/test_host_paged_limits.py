@@ -49,3 +49,11 @@ def test_widths_past_31_bits_change_nothing(kvc):
             for m, p in (((1 << 31) - 1, 1), ((1 << 31) - 1, 1 << 20), ((1 << 31) - 1, 1 << 21))]
     assert wide[0][0] == kvc.KVC_OK and len(set(wide)) == 1
 
+
+def test_items_past_a_launch_are_dealt(kvc):
+    """2^24 items of short sequences are more than a launch has workgroups
+    for: the workspace is that of a dealt call."""
+    st, n = sizes(kvc, **shape(16384, 1024, 1024, max_pages=4))
+    assert st == kvc.KVC_OK and n < 1 << 26
+    st, n = sizes(kvc, **shape(15000, 1000, 1000, max_pages=4))
+    assert st == kvc.KVC_OK and n > 4 * 15000 * 1000
