@@ -133,7 +133,8 @@ __device__ Totals plan(const TableArgs& a, LdsSums* lds) {
         __syncthreads();                        // (behind it, every read of free_in and held_in is done)
     }
     const int64_t taken = base[1], given = base[2], left = count + given - taken;
-    if (count < 0 || count > a.free_capacity) wrong |= 1u;
+    // (places on the stack are 32 bits)
+    if (count < 0 || count > a.free_capacity || count + given > 0x7FFFFFFF) wrong |= 1u;
     if (left < 0 || left > a.free_capacity || rows > static_cast<uint64_t>(a.max_rows)) wrong |= 2u;
     const bool go = !wrong;
     for (int64_t b = tid; b < a.batch; b += kPlanThreads) {

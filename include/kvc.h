@@ -397,8 +397,8 @@ int kvc_decode_paged(const void* h_header, const void* d_in, uint64_t in_bytes,
  *     position / P.  Rows behind the last, up to max_rows, get -1 in both.
  * Entries of the table behind a request's pages are left as they were.
  * On an error (kvc_block_table_result): KVC_ERR_INVALID for a negative length,
- * a held count outside [0, max_pages] or a *d_free_in outside [0,
- * free_capacity]; KVC_ERR_CAPACITY where a request needs more than max_pages
+ * a held count outside [0, max_pages], a *d_free_in outside [0,
+ * free_capacity] or 2^31 free and surplus pages together; KVC_ERR_CAPACITY where a request needs more than max_pages
  * pages or 2^31 tokens, the step more pages than are free, more than max_rows
  * rows, or a trim more than free_capacity entries.  The table, the stack, the
  * held counts and the height are then what they were, every row start is 0
