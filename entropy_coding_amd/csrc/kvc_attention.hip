@@ -501,9 +501,10 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     s.lds_tiles = channels > 128 && (fp8 || usual > 64) ? 1 : 2;
     s.tile_shift = !s.wide ? 4 : s.row_tiles == 1 ? 6 : 7;
     // Long sequences are split.  Of short ones each item gets a workgroup and no join is launched (one token over 512
-    // tokens: 10.2 us instead of 12.4; 200 sequences of up to 500: 61 instead of 108); but each reads the lengths up to
+    // tokens: 10.2 us instead of 12.4; 200 sequences of up to 500: 52 instead of 92); but each reads the lengths up to
     // its own, so that many sequences are dealt to fewer workgroups, which go on where they are (1000 sequences of up
-    // to 300 tokens: 279 us and dealt 247, with six drafted tokens each 338 and 421; 4000 of up to 100: 2117 and 521).
+    // to 300 tokens: 308 us and dealt 223, with six drafted tokens each 387 and 256; 4000 of up to 100: 2117 and 490,
+    // with six 578).
     // (A launch has fewer than 2^32 threads.)
     const uint64_t tile_rows = uint64_t(1) << s.tile_shift;
     const uint64_t items = attend_items(batch, heads, ratio, rows, tile_rows);

@@ -79,8 +79,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
     const uint32_t from = place * plan.per, end = from + plan.per;
     uint32_t at = from;
     bool note = blockIdx.x == 0 && wave == 0;
+    Share sh;
     while (at < end) {
-        Share sh;
         share_of(a, plan, at, &sh, note);
         note = false;
         if (!sh.any) break;
