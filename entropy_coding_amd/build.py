@@ -6,6 +6,7 @@ contraction (-ffp-contract=off), float32 denormals kept
 """
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -27,6 +28,7 @@ DEVICE = [
     "-x", "hip", f"--offload-arch={ARCH}", "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
+RESOURCES = "-Rpass-analysis=kernel-resource-usage"     # (what a kernel takes, as remarks)
 
 
 def hipcc() -> str:
@@ -36,6 +38,24 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def resource_file(src: str) -> str:
+    return os.path.join(HERE, "_build", os.path.splitext(src)[0] + ".resources")
+
+
+def resources(src: str) -> dict:
+    """What the kernels of a source take, as its last build() reported it:
+    {kernel's mangled name: {"VGPRs": ..., "ScratchSize [bytes/lane]": ..., ...}}."""
+    kernels, at = {}, None
+    with open(resource_file(src)) as f:
+        for line in f:
+            key, value = re.search(r"remark:\s*([^:]+): (\S+) \[", line).groups()
+            if key == "Function Name":
+                at = kernels.setdefault(value, {})
+            else:
+                at[key] = int(value) if value.isdigit() else value
+    return kernels
+
+
 def build(verbose: bool = False) -> str:
     cc = hipcc()
     obj_dir = os.path.join(HERE, "_build")
@@ -43,7 +63,7 @@ def build(verbose: bool = False) -> str:
     rocm = os.path.dirname(os.path.dirname(cc))
     host_cxx = shutil.which("g++") or "g++"
     host = ["-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(rocm, "include"), "-Wall", "-Wextra"]
-    steps = [(cc, src, DEVICE) for src in KERNELS]
+    steps = [(cc, src, [*DEVICE, RESOURCES]) for src in KERNELS]
     # the C ABI layer is host code only: plain g++ against the HIP runtime API
     steps += [(host_cxx, src, host) for src in HOST]
 
@@ -53,7 +73,14 @@ def build(verbose: bool = False) -> str:
         cmd = [comp, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        subprocess.run(cmd, check=True)
+        done = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
+        remarks = [x for x in done.stderr.splitlines() if RESOURCES in x]
+        if done.returncode or verbose or not remarks:
+            print(done.stderr, end="", file=sys.stderr)
+        done.check_returncode()
+        if remarks:
+            with open(resource_file(src), "w") as f:
+                f.write("\n".join(remarks) + "\n")
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:

@@ -18,6 +18,18 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;
 constexpr float kNegInf = -__builtin_inff();
 
+// The same number, for the compiler another one: what is computed from it is
+// computed where it is used, not kept in registers over the loop.
+__device__ inline int again(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ inline uint32_t again_uniform(uint32_t x) {
+    x = __builtin_amdgcn_readfirstlane(x);
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
 // ---------------------------------------------------------------- the split
 
 struct Seq {
@@ -53,7 +65,7 @@ __device__ inline Seq seq_of(const AttendArgs& a, uint32_t b) {
 // and what a workgroup takes for its share still lies within one sequence.
 struct Plan {
     uint32_t per;
-    bool aligned;
+    uint32_t aligned;                           // 0 or 1
 
     __device__ static uint32_t tiles(const AttendArgs& a, const Seq& s) {
         return (uint32_t(s.rows) * a.ratio + (1u << a.tile_shift) - 1) >> a.tile_shift;
@@ -64,9 +76,9 @@ struct Plan {
     __device__ uint32_t units(uint32_t real) const { return aligned ? (real + per - 1) / per * per : real; }
 };
 
-__device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
-    Plan p{1, false};
-    if (!a.split) return p;                     // an item a workgroup
+__device__ inline Plan split_plan(const AttendArgs& a, uint32_t least) {
+    Plan p;
+    p.aligned = 0;
     const uint32_t lane = threadIdx.x & 63;
     // the first 64 sequences' items and units, kept for all sums
     uint32_t items0 = 0, real0 = 0;
@@ -91,15 +103,21 @@ __device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
     uint32_t per = (units + a.target - 1) / a.target;
     if (per < least) per = least;
     p.per = per;
-    if (of_lane(scan(all), 63) > a.target) return p;
-    for (int i = 0; i < 2 && !p.aligned; ++i, per += (per + 7) / 8) {
+    const bool fits = of_lane(scan(all), 63) <= a.target;
+    for (int i = 0; fits && i < 2 && !p.aligned; ++i, per += (per + 7) / 8) {
         uint32_t groups = 0;
         each([&](uint32_t items, uint32_t real) { groups += items * ((real + per - 1) / per); });
         if (of_lane(scan(groups), 63) > a.target) continue;
-        p.aligned = true;
+        p.aligned = 1;
         p.per = per;
     }
     return p;
+}
+
+__device__ inline Plan plan_of(const AttendArgs& a, uint32_t least) {
+    Plan p{1, 0};                               // an item a workgroup
+    if (a.split) p = split_plan(a, least);
+    return Plan{uint32_t(__builtin_amdgcn_readfirstlane(p.per)), uint32_t(__builtin_amdgcn_readfirstlane(p.aligned))};
 }
 
 // The item that holds a unit, and where it lies.
@@ -125,7 +143,7 @@ __device__ inline void item_of(Share* r, uint32_t at) {
 // and the flags.
 __device__ inline void share_of(const AttendArgs& a, const Plan& p, uint32_t at, Share* r, bool note) {
     if (r->any && at < r->past) return item_of(r, at);
-    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t lane = again(threadIdx.x & 63);
     uint32_t base = r->base;
     bool bad = false;
     r->any = false;
@@ -166,13 +184,13 @@ __device__ inline void share_of(const AttendArgs& a, const Plan& p, uint32_t at,
     if (note) {
         bad = __any(bad);
         if (lane == 0) {
-            a.ctl->magic = kPagedMagic;
+            a.ctl->magic = again_uniform(kPagedMagic);
             a.ctl->flags = bad ? kPagedInvalid : 0u;
             a.ctl->grid = gridDim.x;
             a.ctl->words_offset =
                 static_cast<uint32_t>(reinterpret_cast<char*>(a.words) - reinterpret_cast<char*>(a.ctl));
-            a.ctl->per = p.per;
-            a.ctl->aligned = p.aligned;
+            a.ctl->per = again_uniform(p.per);
+            a.ctl->aligned = again_uniform(p.aligned);
         }
     }
 }

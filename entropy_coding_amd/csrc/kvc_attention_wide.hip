@@ -18,13 +18,17 @@
 // instructions of 16 cycles and about as many cycles of vector instructions
 // (32 exponentials at 16 cycles, 150 others at 4), and the two waves that a
 // SIMD holds overlap them in part.  Two pieces of 1000 tokens behind 7001
-// cached ones (8 KV heads, 4 query heads each, bf16: 246 GFLOP) take 270 to
-// 282 us, 870 to 910 TFLOP/s, where a library's large matrix product reaches
-// 1390 on the same card; matrix units busy 32% of the time, vector units 35%,
-// LDS 25% without conflicts.  RT = 4 needs registers that a wave does not have, and 64 rows
+// cached ones (8 KV heads, 4 query heads each, bf16: 246 GFLOP) take 263 to
+// 277 us, 890 to 930 TFLOP/s, where a library's large matrix product reaches
+// 1390 on the same card.  RT = 4 needs registers that a wave does not have, and 64 rows
 // (RT = 1) read each operand from LDS for half as many products.  Tried and
 // slower: the tile after the next on its way too (4 sequences of 16 drafted
 // tokens over 4096: 30.2 us instead of 28.3).
+//
+// Registers are what there is least of: 250 of the 256 that two workgroups a
+// CU leave a wave.  No variant keeps any in scratch memory: what only a tile
+// that is masked or an item's end needs is formed there (`again`), not before
+// the loop over tiles, and in the fullest variants a lane's place in a tile too.
 #include "kvc_attend_device.hpp"
 
 #include <type_traits>
@@ -39,7 +43,8 @@ constexpr int kNoDs = 0x7F;                     // the scheduler may move all ac
 
 // Workgroups (of a wave a SIMD) that a CU can hold at once: by the registers
 // of a wave (sums, queries, scores, weights, the staged quarter of a tile and
-// about 80 for the rest, of 512) and by the tiles in 160 KB of LDS.
+// up to 80 for the rest, of 512: bf16 of 256 channels is counted as 264 and
+// takes less than 256 in fact) and by the tiles in 160 KB of LDS.
 constexpr int groups_of(int d, bool fp8, int rt, int bufs) {
     const int need = d * rt / 4 + d * rt / 8 + 16 * rt + 8 * rt + d * (fp8 ? 1 : 2) / 8 + 80;
     const int regs = need <= 168 ? 3 : need <= 264 ? 2 : 1;
@@ -51,7 +56,19 @@ template <int D, int BUFS>
 struct WideLds {
     u32x4 k[BUFS][4 * (D / 32)][64];
     u32x4 v[BUFS][2 * (D / 16)][64];
+    u32x4 said;                                 // a word a wave
 };
+
+// Whether any of the workgroup's waves has x (one value a wave).  The vote
+// over all threads that the runtime offers keeps the packed thread numbers in
+// a register over the whole kernel.
+__device__ inline bool any_wave(bool x, u32x4& said, int wave) {
+    if ((threadIdx.x & 63) == 0) reinterpret_cast<uint32_t*>(&said)[wave] = x;
+    __syncthreads();
+    const u32x4 all = said;
+    __syncthreads();                            // (read before the next vote writes)
+    return (all[0] | all[1] | all[2] | all[3]) != 0;
+}
 
 // PAGE: 16, 4 or 1, the largest that divides the tokens of a page: with 16 a
 // half of a wave's 32 tokens lies in one page, its rows a constant stride
@@ -66,11 +83,12 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
     constexpr int KK = D / 32;                  // products over the channels
     constexpr int N4 = 2 * KG;                  // 16-byte registers a lane stages, of K or of V
     constexpr int VS = PAGE == 1 ? 8 : 2;
+    // whether a lane's place in a tile keeps its registers: where there are none left it is formed for each tile
+    constexpr bool KEEP = FP8 || !((D == 256 && BUFS == 1) || (D == 128 && RT == 2 && PAGE == 1));
     __shared__ WideLds<D, BUFS> lds;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, q4 = lane >> 4;
     const bool is_v = wave >= 2;
     const uint32_t place = place_of(blockIdx.x, gridDim.x);
     const Plan plan = plan_of(a, 1);
@@ -96,14 +114,13 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
         const int32_t* const table = a.block_table + int64_t(sh.b) * a.max_pages;
 
         bf16x8 qf[RT][KK];
-        int node[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const Query query(a, sh, row0 + rt * 64 + n, pt.rows);
-            node[rt] = query.node;
+            const Query query(a, sh, row0 + rt * 64 + (again(lane) & 15), pt.rows);
+            const int part = (again(lane) >> 4);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                qf[rt][kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk & 1) : 32 * kk + 8 * q4, sc.flip);
+                qf[rt][kk] = query.at(FP8 ? 64 * (kk / 2) + 16 * part + 8 * (kk & 1) : 32 * kk + 8 * part, sc.flip);
         }
         f32x4 o[RT][C];
         RowSum row[RT];
@@ -115,7 +132,12 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
         // Staging.  A wave has 32 tokens of a tile: a lane of K token n of both halves, a lane of V a run of four of
         // each half.  Page numbers are read a tile ahead of the rows.
         const int half32 = (wave & 1) * 32;
-        auto token = [&](int t, int i) -> uint32_t {
+        // This lane's place in that, kept or formed for each tile anew.
+        const int kept_n = lane & 15, kept_q4 = lane >> 4;
+        auto place_n = [&]() -> int { return KEEP ? kept_n : again(lane) & 15; };
+        auto place_q4 = [&]() -> int { return KEEP ? kept_q4 : again(lane) >> 4; };
+        auto stages_v = [&]() -> bool { return KEEP ? is_v : again_uniform(wave) >= 2; };
+        auto token = [&](int t, int i, int n, int q4) -> uint32_t {
             const int x = t * kWideTile + half32 +
                           (PAGE == 16 ? 16 * i : is_v ? (VS == 2 ? 16 * i : (i < 4 ? 0 : 12) + i) + q4 * 4 : 16 * (i & 1) + n);
             return static_cast<uint32_t>(x < length ? x : PAGE == 16 ? (length - 1) & ~15
@@ -123,21 +145,24 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
         };
         int32_t page[VS];
         auto read_pages = [&](int t) {
+            const int n = place_n(), q4 = place_q4();
 #pragma unroll
             for (int i = 0; i < VS; ++i) {
-                const int32_t* const at_page = table + page_index(a, token(t, i));
+                const int32_t* const at_page = table + page_index(a, token(t, i, n, q4));
                 page[i] = PAGE == 16 ? uniform_word(at_page) : *at_page;
             }
         };
-        auto row_at = [&](int t, int i) -> uint64_t {
-            return uint64_t(slot_in(a, page[i], token(t, i), &bad_page)) * row_bytes;
-        };
         u32x4 st[N4];
         auto load = [&](int t) {
+            const int n = place_n(), q4 = place_q4();
+            const bool is_v = stages_v();
+            auto row_at = [&](int i) -> uint64_t {
+                return uint64_t(slot_in(a, page[i], token(t, i, n, q4), &bad_page)) * row_bytes;
+            };
             if (is_v) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const GlobalBytes p = pool + row_at(t, VS == 2 ? j / 4 : j) +
+                    const GlobalBytes p = pool + row_at(VS == 2 ? j / 4 : j) +
                                           ((PAGE == 16 ? q4 * 4 + (j & 3) : PAGE == 4 ? j & 3 : 0) * row_bytes +
                                            uint32_t(n) * (C * ES));
                     Words<VW> w;
@@ -148,7 +173,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
             } else {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const GlobalBytes p = pool + row_at(t, hf) + ((PAGE == 16 ? n * row_bytes : 0u) + 16u * q4);
+                    const GlobalBytes p = pool + row_at(hf) + ((PAGE == 16 ? n * row_bytes : 0u) + 16u * q4);
 #pragma unroll
                     for (int kg = 0; kg < KG; ++kg)
                         st[hf * KG + kg] = *reinterpret_cast<const KVC_GLOBAL u32x4*>(p + 64 * kg);
@@ -157,14 +182,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
         };
         bool any_wild = false;
         auto write = [&](int t, int buf) {
-            if (is_v) {
+            if (stages_v()) {
                 const int t0 = t * kWideTile + half32;
                 if (t0 + 32 > ctx) {
                     // tokens behind the last one are cleared, and infinities and NaN of drafted ones
                     uint32_t wild = 0;
+                    const int first = (again(lane) >> 4) * 4;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int tok = t0 + (j < 4 ? 0 : 12) + q4 * 4 + j;
+                        const int tok = t0 + (j < 4 ? 0 : 12) + first + j;
                         const uint32_t there = tok < length ? ~0u : 0u, drafted = tok >= ctx ? ~0u : 0u;
 #pragma unroll
                         for (int x = 0; x < VW; ++x) {
@@ -230,7 +256,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
             if (t0 + kWideTile > pt.full) {
 #pragma unroll
                 for (int rt = 0; rt < G; ++rt) {
-                    const uint64_t win = window_of(a, sh.seq.start, node[rt], t0 - ctx, length - ctx) >> (q4 * 4);
+                    const int node = Query(a, sh, row0 + rt * 64 + (again(lane) & 15), pt.rows).node;
+                    const uint64_t win = window_of(a, sh.seq.start, node, t0 - ctx, length - ctx) >> ((again(lane) >> 4) * 4);
 #pragma unroll
                     for (int hf = 0; hf < 4; ++hf)
 #pragma unroll
@@ -272,6 +299,9 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
                     pf[rt][st2] = frag_of(two_bf16(e[0], e[1]), two_bf16(e[2], e[3]), two_bf16(e[4], e[5]), two_bf16(e[6], e[7]));
                 }
             }
+            // (Left to itself the scheduler draws the exponentials in among the products, and the reads back to one ahead of
+            // theirs: the pieces above in pages of 12 tokens 298 us instead of 281, of 16 tokens 275 and 270.)
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < 2 * C; ++i) {
                 const int st2 = i / C, c = i % C;
@@ -280,7 +310,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
                 for (int rt = 0; rt < G; ++rt)
                     o[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][st2], o[rt][c], 0, 0, 0);
                 if (i + kAhead < 2 * C) ring[i % kAhead] = lds.v[buf][i + kAhead][lane];
-                __builtin_amdgcn_sched_barrier(kNoDs);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
@@ -303,7 +333,7 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
                 __syncthreads();
             }
         }
-        any_wild = __syncthreads_or(any_wild);
+        any_wild = any_wave(any_wild, lds.said, wave);
 
         // each wave has its rows' sums: lane l those of row n, channels 4 q C .. 4 (q + 1) C - 1
 #pragma unroll
@@ -311,14 +341,15 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
             float sum = row[rt].sum;
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            const int m = row0 + rt * 64 + n;
+            const int m = row0 + rt * 64 + (again(lane) & 15), at_ch = (again(lane) >> 4) * 4 * C;
             if (m < pt.rows) {
+                const int node = m / static_cast<int>(a.ratio);
                 const float best = row[rt].top();
                 if (pt.whole) {
-                    const int64_t out_row = int64_t(sh.seq.start) + node[rt];
-                    const int64_t head = int64_t(sh.head) * a.ratio + (m - node[rt] * static_cast<int>(a.ratio));
+                    const int64_t out_row = int64_t(sh.seq.start) + node;
+                    const int64_t head = int64_t(sh.head) * a.ratio + (m - node * static_cast<int>(a.ratio));
                     const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-                    uint16_t* const out = a.out + out_row * a.out_row + head * D + q4 * 4 * C;
+                    uint16_t* const out = a.out + out_row * a.out_row + head * D + at_ch;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -326,19 +357,19 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
                             *reinterpret_cast<uint2*>(out + i * C + c) =
                                 uint2{two_bf16(o[rt][c][i] * inv, o[rt][c + 1][i] * inv),
                                       two_bf16(o[rt][c + 2][i] * inv, o[rt][c + 3][i] * inv)};
-                    if (a.lse && q4 == 0)
+                    if (a.lse && lane < 16)
                         a.lse[out_row * (int64_t(a.heads) * a.ratio) + head] =
                             sum == 0.0f ? kNegInf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
                 } else {
                     const uint64_t to = (uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0);
-                    float* const out = a.partial + to * D + q4 * 4 * C;
+                    float* const out = a.partial + to * D + at_ch;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int c = 0; c < C; c += 4)
                             *reinterpret_cast<f32x4*>(out + i * C + c) =
                                 f32x4{o[rt][c][i], o[rt][c + 1][i], o[rt][c + 2][i], o[rt][c + 3][i]};
-                    if (q4 == 0) *reinterpret_cast<float2*>(a.pairs + 2 * to) = float2{best, sum};
+                    if (lane < 16) *reinterpret_cast<float2*>(a.pairs + 2 * to) = float2{best, sum};
                 }
             }
         }
@@ -347,17 +378,18 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
             const GlobalBytes vp =
                 reinterpret_cast<GlobalBytes>(reinterpret_cast<uintptr_t>(a.pools[1])) + sh.head * (D * ES);
             const int last = tb * kWideTile < length ? tb * kWideTile : length;
-            for (int m = row0 + n; m < pt.rows && m < row0 + 64 * RT; m += 64) {
+            const int at_ch = (again(lane) >> 4) * 4 * C;
+            for (int m = row0 + (again(lane) & 15); m < pt.rows && m < row0 + 64 * RT; m += 64) {
                 const int nd = m / static_cast<int>(a.ratio);
                 const int64_t out_row = int64_t(sh.seq.start) + nd;
                 const int64_t head = int64_t(sh.head) * a.ratio + (m - nd * static_cast<int>(a.ratio));
-                uint16_t* const out = a.out + out_row * a.out_row + head * D + q4 * 4 * C;
-                float* const part = a.partial + ((uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0)) * D + q4 * 4 * C;
+                uint16_t* const out = a.out + out_row * a.out_row + head * D + at_ch;
+                float* const part = a.partial + ((uint64_t(pt.slot) << a.tile_shift) + (m - pt.row0)) * D + at_ch;
                 for (int tok = ta * kWideTile > ctx ? ta * kWideTile : ctx; tok < last; ++tok) {
                     if (!sees(a, sh.seq.start, nd, static_cast<uint32_t>(tok - ctx))) continue;
                     uint32_t known = 0;
                     const GlobalBytes p =
-                        vp + uint64_t(slot_in(a, table[page_index(a, tok)], tok, &known)) * row_bytes + q4 * 4 * (C * ES);
+                        vp + uint64_t(slot_in(a, table[page_index(a, tok)], tok, &known)) * row_bytes + at_ch * ES;
                     for (int c = 0; c < 4 * C; ++c) {
                         const uint32_t w = *reinterpret_cast<const KVC_GLOBAL uint32_t*>(p + 4 * (c * ES / 4));
                         const float x = wild_part<FP8>(w, c);
@@ -369,8 +401,8 @@ __global__ __launch_bounds__(64 * kWaves, groups_of(D, FP8, RT, BUFS)) void k_at
             }
         }
     }
-    const uint32_t any = __syncthreads_or(static_cast<int>(bad_page));
-    if (threadIdx.x == 0) a.words[blockIdx.x] = any ? kPagedInvalid : 0u;
+    const bool any = any_wave(__any(bad_page != 0), lds.said, wave);
+    if (wave == 0 && again(lane) == 0) a.words[blockIdx.x] = any ? kPagedInvalid : 0u;
 }
 
 template <int D, bool FP8, int RT, int BUFS, int PAGE>
