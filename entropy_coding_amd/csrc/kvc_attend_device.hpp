@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "kvc_paged.hpp"
+#include "kvc_split.hpp"
 #include "kvc_wave.hpp"
 
 namespace kvc {
@@ -63,18 +64,10 @@ __device__ inline Seq seq_of(const AttendArgs& a, uint32_t b) {
 // kept between calls).  unit_shift is such that the units of a call whose row
 // starts are prefix sums stay below 2^31; where they are not, sums may wrap,
 // and what a workgroup takes for its share still lies within one sequence.
-struct Plan {
-    uint32_t per;
-    uint32_t aligned;                           // 0 or 1
-
-    __device__ static uint32_t tiles(const AttendArgs& a, const Seq& s) {
-        return (uint32_t(s.rows) * a.ratio + (1u << a.tile_shift) - 1) >> a.tile_shift;
-    }
-    __device__ static uint32_t real(const AttendArgs& a, const Seq& s) {
-        return !a.split ? 1u : (uint32_t(s.context) + uint32_t(s.rows) + (1u << a.unit_shift) - 1) >> a.unit_shift;
-    }
-    __device__ uint32_t units(uint32_t real) const { return aligned ? (real + per - 1) / per * per : real; }
-};
+__device__ inline uint32_t tiles_of(const AttendArgs& a, const Seq& s) { return row_tiles(s.rows, a.ratio, a.tile_shift); }
+__device__ inline uint32_t real_of(const AttendArgs& a, const Seq& s) {
+    return !a.split ? 1u : units_in(uint32_t(s.context) + uint32_t(s.rows), a.unit_shift);
+}
 
 __device__ inline Plan split_plan(const AttendArgs& a, uint32_t least) {
     Plan p;
@@ -84,14 +77,14 @@ __device__ inline Plan split_plan(const AttendArgs& a, uint32_t least) {
     uint32_t items0 = 0, real0 = 0;
     if (lane < a.batch) {
         const Seq s = seq_of(a, lane);
-        items0 = Plan::tiles(a, s) * a.heads;
-        real0 = Plan::real(a, s);
+        items0 = tiles_of(a, s) * a.heads;
+        real0 = real_of(a, s);
     }
     auto each = [&](auto add) {                 // the items and units of this lane's sequences
         add(items0, real0);
         for (uint32_t b = 64 + lane; b < a.batch; b += 64) {
             const Seq s = seq_of(a, b);
-            add(Plan::tiles(a, s) * a.heads, Plan::real(a, s));
+            add(tiles_of(a, s) * a.heads, real_of(a, s));
         }
     };
     uint32_t units = 0, all = 0;
@@ -100,13 +93,12 @@ __device__ inline Plan split_plan(const AttendArgs& a, uint32_t least) {
         all += items;
     });
     units = of_lane(scan(units), 63);
-    uint32_t per = (units + a.target - 1) / a.target;
-    if (per < least) per = least;
+    uint32_t per = first_per(units, a.target, least);
     p.per = per;
     const bool fits = of_lane(scan(all), 63) <= a.target;
-    for (int i = 0; fits && i < 2 && !p.aligned; ++i, per += (per + 7) / 8) {
+    for (int i = 0; fits && i < 2 && !p.aligned; ++i, per = next_per(per)) {
         uint32_t groups = 0;
-        each([&](uint32_t items, uint32_t real) { groups += items * ((real + per - 1) / per); });
+        each([&](uint32_t items, uint32_t real) { groups += items * groups_in(real, per); });
         if (of_lane(scan(groups), 63) > a.target) continue;
         p.aligned = 1;
         p.per = per;
@@ -132,10 +124,10 @@ struct Share {
 };
 
 __device__ inline void item_of(Share* r, uint32_t at) {
-    const uint32_t item = (at - r->begin) / r->units;
-    r->head = __builtin_amdgcn_readfirstlane(item / r->tiles);
-    r->tile = __builtin_amdgcn_readfirstlane(item - r->head * r->tiles);
-    r->first = __builtin_amdgcn_readfirstlane(r->begin + item * r->units);
+    const Item i = item_at(r->begin, r->units, r->tiles, at);
+    r->head = __builtin_amdgcn_readfirstlane(i.head);
+    r->tile = __builtin_amdgcn_readfirstlane(i.tile);
+    r->first = __builtin_amdgcn_readfirstlane(i.first);
 }
 
 // Finds the item that holds unit `at`, not before what *r holds: it is looked
@@ -154,8 +146,8 @@ __device__ inline void share_of(const AttendArgs& a, const Plan& p, uint32_t at,
         if (b < a.batch) {
             s = seq_of(a, b);
             bad = bad || s.bad;
-            tiles = Plan::tiles(a, s);
-            real = Plan::real(a, s);
+            tiles = tiles_of(a, s);
+            real = real_of(a, s);
         }
         const uint32_t u = p.units(real);
         const uint32_t count = tiles * a.heads * u;
@@ -351,33 +343,21 @@ struct Part {
     uint32_t slot;                              // else: where the part goes
 };
 
-// Of an item's `tiles` tiles, those before its unit `done`.  As a rule a unit
-// is a tile; where they differ (a chain's rows that see less than the whole
-// sequence, units of many tiles) the tiles are spread over the units, exact
-// at both ends: products stay below 2^53.
-__device__ inline int tiles_before(uint32_t tiles, uint32_t done, uint32_t units) {
-    if (done >= units) return static_cast<int>(tiles);
-    if (tiles == units) return static_cast<int>(done);
-    return __builtin_amdgcn_readfirstlane(static_cast<int>(double(tiles) * double(done) / double(units)));
-}
-
 __device__ inline Part part_of(const AttendArgs& a, const Share& sh, uint32_t place, uint32_t at, uint32_t from,
                                uint32_t end, uint32_t unit) {
     Part r;
-    const int tile_rows = 1 << a.tile_shift;
     r.rows = sh.seq.rows * static_cast<int>(a.ratio);
     r.row0 = static_cast<int>(sh.tile << a.tile_shift);
     r.context = sh.seq.context;
-    // a chain's rows see nothing behind their last token, and all up to their first
-    const int last = (r.row0 + tile_rows < r.rows ? r.row0 + tile_rows : r.rows) - 1;
-    r.length = r.context + (a.mask ? sh.seq.rows : last / static_cast<int>(a.ratio) + 1);
-    r.full = r.context + (a.mask ? 0 : r.row0 / static_cast<int>(a.ratio) + 1);
-    const uint32_t tiles = (static_cast<uint32_t>(r.length) + unit - 1) / unit;
-    const uint32_t past = sh.first + sh.units;
-    r.whole = sh.first >= from && past <= end;
-    r.slot = 2 * place + (sh.first >= from ? 1u : 0u);
-    r.ta = tiles_before(tiles, at - sh.first, sh.real);
-    r.tb = tiles_before(tiles, (past < end ? past : end) - sh.first, sh.real);
+    const Extent e = extent_of(!a.mask, r.context, sh.seq.rows, r.rows, r.row0, 1 << a.tile_shift, static_cast<int>(a.ratio));
+    r.length = e.length;
+    r.full = e.full;
+    const Range g = range_of(sh.first, sh.units, sh.real, (static_cast<uint32_t>(r.length) + unit - 1) / unit, place, at,
+                             from, end);
+    r.whole = g.whole;
+    r.slot = g.slot;
+    r.ta = g.ta;
+    r.tb = g.tb;
     return r;
 }
 

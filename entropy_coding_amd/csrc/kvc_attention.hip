@@ -441,11 +441,11 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a, uint32_t grid
         const uint32_t tile = m >> a.tile_shift;
         if (tile >= span.tiles) continue;
         const uint32_t first = span.base + (h * span.tiles + tile) * span.units;
-        const uint32_t w0 = first / per, w1 = (first + span.units - 1) / per;
-        if (w0 >= w1 || w1 >= grid) continue;
-        const uint32_t parts = w1 - w0 + 1;
+        const Sharers who = sharers_of(first, span.units, per);
+        if (who.first >= who.last || who.last >= grid) continue;
+        const uint32_t parts = who.last - who.first + 1;
         const uint32_t lr = m - (tile << a.tile_shift);
-        auto place = [&](uint32_t s) { return (uint64_t(2 * (w0 + s) + (s ? 0 : 1)) << a.tile_shift) + lr; };
+        auto place = [&](uint32_t s) { return (uint64_t(who.slot(s)) << a.tile_shift) + lr; };
         Joined<D> j;
         if (parts <= 4) j.template add<4>(a, lane, parts, place);
         else j.template add<E <= 2 ? 16 : 8>(a, lane, parts, place);
