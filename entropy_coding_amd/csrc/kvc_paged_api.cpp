@@ -87,8 +87,9 @@ int64_t widest_of(const kvc_paged_kv* g) {
 kvc::AttendShape shape_of(const kvc_paged_kv* g, const kvc_attention* p) {
     const int64_t widest = widest_of(g);
     const int64_t longest = p->max_tokens > 0 && p->max_tokens < widest ? p->max_tokens : widest;
+    const int64_t usual = p->rows_per_sequence < 1 << 24 ? p->rows_per_sequence : 1 << 24;    // (more than any has)
     return kvc::attend_shape(g->batch, g->heads, p->q_heads / g->heads, p->channels, p->kv_dtype == KVC_E4M3, p->rows,
-                             p->rows_per_sequence, longest, widest);
+                             usual, longest, widest);
 }
 
 }  // namespace

@@ -57,3 +57,11 @@ def test_items_past_a_launch_are_dealt(kvc):
     assert st == kvc.KVC_OK and n < 1 << 26
     st, n = sizes(kvc, **shape(15000, 1000, 1000, max_pages=4))
     assert st == kvc.KVC_OK and n > 4 * 15000 * 1000
+
+
+@pytest.mark.parametrize("hint", [1 << 24, 1 << 40, (1 << 61) + 1, (1 << 63) - 1])
+def test_any_usual_number_of_rows(kvc, hint):
+    """A hint of more rows than there can be is one of many rows."""
+    for ratio in (1, 4, 1000):
+        f = shape(2, 3, 4000 if ratio < 1000 else 20, ratio, max_pages=1000)
+        assert sizes(kvc, **dict(f, rows_per_sequence=hint)) == sizes(kvc, **dict(f, rows_per_sequence=1 << 20))
