@@ -491,6 +491,11 @@ class PagedKV:
         self.kv_dtype = _kv_dtype(pools[0])
         self.ref = ctypes.byref(self.desc)
         self._own = (torch._C._cuda_getCurrentRawStream(block_table.device.index), self.ptrs)
+        self._aligned = all(t.data_ptr() % 16 == 0 for t in pools)
+
+    def _check_pools(self):
+        if not self._aligned:
+            raise ValueError("the pools must be 16-byte aligned")
 
 
 def kvc_decode_paged(stream_bytes, mu, sigma, prefix, paged: PagedKV, workspace, stream=None,
@@ -639,6 +644,7 @@ def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tenso
     wider rows allowed) to the slots [rows] (int64; -1: none) of one layer's
     pages; bf16 rows of an e4m3 cache are rounded from x / scale."""
     dev = paged.block_table.device
+    paged._check_pools()
     rows = slots.shape[0]
     _tensor(slots, "slots", torch.int64, (None,), dev)
     heads, ch = paged.desc.heads, paged.channels
@@ -663,6 +669,7 @@ class PagedAttention:
 
     def __init__(self, paged: PagedKV, q_heads: int, max_rows: int, rows_per_sequence: int = 0, max_tokens: int = 0,
                  softmax_scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0):
+        paged._check_pools()
         self.paged, self.q_heads, self.max_rows = paged, q_heads, max_rows
         self.device = paged.block_table.device
         self.batch, ch = paged.desc.batch, paged.channels

@@ -452,7 +452,7 @@ int kvc_block_table_result(const void* d_workspace, void* stream, int64_t* h_row
  * float32 quotient x / k_scale (x / v_scale) rounded to nearest even, what lies beyond +-448
  * saturated, NaN kept.  Scales are finite and positive, and 1 when the types
  * are the same.  h_paged as for kvc_decode_paged (its table is not read and
- * may be NULL).  d_k and d_v 16-byte aligned, row strides (in values, at
+ * may be NULL), its pools 16-byte aligned.  d_k and d_v 16-byte aligned, row strides (in values, at
  * least heads x channels; not looked at for one row) such that every row is.  Does not
  * synchronise; KVC_ERR_INVALID for bad arguments, nothing launched.
  */
@@ -482,7 +482,8 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * maxima and the output's accumulation are float32; the weights are rounded
  * to bf16 for the matrix instructions, the output to bf16.  Rows behind
  * d_row_starts[batch] are left as they were.
- * q and out bf16, the cache bf16 or e4m3; channels 64, 128, 192 or 256;
+ * q and out bf16, the cache bf16 or e4m3, its pools 16-byte aligned;
+ * channels 64, 128, 192 or 256;
  * q_heads a multiple of heads, at most 1024 per KV head, rows x q_heads <
  * 2^31; at most 16384 sequences; heads x (rows x (q_heads / heads) / 16 +
  * min(rows, batch)) < 2^30; num_pages x page_tokens < 2^31;

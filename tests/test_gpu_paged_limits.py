@@ -43,3 +43,23 @@ def test_a_stack_of_31_bits_with_surplus_pages(kvc, cuda):
     assert tab.result() == 20
     assert int(count) == (1 << 31) - 3 and held.tolist() == [1, 2] and table.tolist()[1][:2] == [8, 9]
     assert slots[:20].tolist() == [8 * 16 + i for i in range(16)] + [9 * 16 + i for i in range(4)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_pools_that_are_not_16_byte_aligned_are_refused(kvc, cuda, kind):
+    """Rows are written, and K is read, 16 bytes at a time."""
+    dtype = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn
+    flat = [torch.zeros(4 * 16 * 2 * 64 + 8, dtype=dtype, device=cuda) for _ in range(2)]
+    k = torch.zeros((1, 2, 64), dtype=dtype, device=cuda)
+    slots, table = torch.zeros(1, dtype=torch.int64, device=cuda), torch.zeros((1, 4), dtype=torch.int32, device=cuda)
+    for first, good in ((0, True), (1, False), (4, False)):
+        pools = [flat[0][:4 * 16 * 2 * 64].view(4, 16, 2, 64), flat[1][first:first + 4 * 16 * 2 * 64].view(4, 16, 2, 64)]
+        paged = kvc.PagedKV(pools, table, 16)
+        if good:
+            kvc.kvc_paged_append(paged, 0, k, k, slots)
+            kvc.PagedAttention(paged, 2, 1)
+            continue
+        with pytest.raises(ValueError):
+            kvc.kvc_paged_append(paged, 0, k, k, slots)
+        with pytest.raises(ValueError):
+            kvc.PagedAttention(paged, 2, 1)
