@@ -27,10 +27,10 @@
 // The weights' rounding to bf16 is what the matrix instruction takes; their
 // sum l is of the unrounded ones, in float32.
 //
-// What bounds it: reading K and V once.  A long cache gets more than 5 TB/s
-// (a copy of 2 GiB 4.9, read and written); the next tokens of 4 sequences of
-// 4096 (8 KV heads, 4 query heads each, 128 channels, bf16: 67 MB) take 20.8
-// us, 16.3 of them here, 4.2 in the join: each wave has six tiles, which is
+// What bounds it: reading K and V once.  The next tokens of 4 sequences of
+// 4096 (8 KV heads, 4 query heads each, 128 channels, bf16: 67 MB) take 20.9
+// us, 16.4 of them here (4.1 TB/s; a copy of 2 GiB 4.9, read and written), 4.4
+// in the join: a workgroup has nine tiles and a wave two or three, which is
 // too few to hide the start (lengths, page numbers, the first K and V, each
 // read waiting for the one before).  One token over 512 tokens: 10.6 us, a
 // chain of such reads.
@@ -495,7 +495,7 @@ AttendShape attend_shape(int64_t batch, int64_t heads, int64_t ratio, int64_t ch
     // two (two pieces of 1000 tokens over 7001 with 192 channels: bf16 997 and 767 us, e4m3 781 and 620; with 256 and one
     // workgroup 1287, two 839).  In bf16 that second workgroup is paid for with registers, so that up to 64 rows, which
     // wait for K and V, keep one (two sequences of 32000 tokens, 192 channels: 56 and 62 us, 256: 67 and 80; but 32 of up
-    // to 4096, 192 channels: 124 and 103); e4m3 gains there as well (67 and 49; 52 and 53; 135 and 78).  A third
+    // to 4096, 192 channels: 124 and 103); e4m3 gains there, or loses nothing (67 and 49; 52 and 53; 135 and 78).  A third
     // workgroup by the same means, e4m3 of 128 channels: 57 and 49 us, but with 4 sequences 26 and 29.
     s.row_tiles = !s.wide || usual <= 64 || channels > 128 ? 1 : 2;
     s.lds_tiles = channels > 128 && (fp8 || usual > 64) ? 1 : 2;

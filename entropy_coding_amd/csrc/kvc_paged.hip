@@ -14,7 +14,7 @@ namespace {
 // pages to give back lie; from them every row finds its request by bisection,
 // and every slot, table entry and push follows by itself (Stack below).  A
 // small step is bound by a chain of reads and barriers in one workgroup: 8
-// requests 6.0 us (the launch alone 3.3), where two launches took 8.2; the
+// requests 6.5 us (the launch alone 3.3), where two launches took 8.2; the
 // sums and the rows of 256 requests with trees 12.8 us in two launches; 64
 // prompts of up to 32768 tokens (1.3 million slots and positions, 16 MB)
 // 12.0 us, 3.1 of them the sums.

@@ -478,10 +478,10 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * (NaN, infinity) at tokens that a row does not see has no part in it; an
  * infinity in V of a drafted token that it sees is one in the output, however
  * small its weight (of a context token whose weight is 0 in float32 it may be
- * NaN).  Sums,
- * maxima and the output's accumulation are float32; the weights are rounded
- * to bf16 for the matrix instructions, the output to bf16.  Rows behind
- * d_row_starts[batch] are left as they were.
+ * NaN).  Sums, maxima and the output's accumulation are float32; the weights
+ * are rounded to bf16 for the matrix instructions, the output to bf16.  V is
+ * summed with weights of up to 2^8 before the division: what passes 3.4e38
+ * then is infinite.  Rows behind d_row_starts[batch] are left as they were.
  * q and out bf16, the cache bf16 or e4m3, its pools 16-byte aligned;
  * channels 64, 128, 192 or 256;
  * q_heads a multiple of heads, at most 1024 per KV head, rows x q_heads <
@@ -494,7 +494,7 @@ int kvc_paged_append(const kvc_paged_kv* h_paged, int64_t layer, int32_t kv_dtyp
  * Does not synchronise.  kvc_paged_attention_result gives KVC_ERR_INVALID
  * where a sequence's row starts fall or pass `rows`, its context is negative
  * or it passes max_pages x page_tokens tokens (that sequence's rows are not
- * written), or where a page number read lies outside [0, num_pages) (page 0 is
+ * written; where row starts fall, others' may not be either), or where a page number read lies outside [0, num_pages) (page 0 is
  * read in its place: its rows are undefined).
  * Workspace: kvc_paged_attention_sizes, 256-byte aligned.
  */
