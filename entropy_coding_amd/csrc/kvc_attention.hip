@@ -27,13 +27,13 @@
 // The weights' rounding to bf16 is what the matrix instruction takes; their
 // sum l is of the unrounded ones, in float32.
 //
-// What bounds it: reading K and V once.  The next tokens of 4 sequences of
-// 4096 (8 KV heads, 4 query heads each, 128 channels, bf16: 67 MB) take 20.9
-// us, 16.4 of them here (4.1 TB/s; a copy of 2 GiB 4.9, read and written), 4.4
-// in the join: a workgroup has nine tiles and a wave two or three, which is
-// too few to hide the start (lengths, page numbers, the first K and V, each
-// read waiting for the one before).  One token over 512 tokens: 10.6 us, a
-// chain of such reads.
+// What bounds it: reading K and V once.  The next tokens of 64 sequences of
+// 4000 (8 KV heads, 4 query heads each, 128 channels, bf16: 1.05 GB) take 196
+// us, 5.3 TB/s (a copy of 2 GiB 4.9, read and written).  Those of 4 sequences
+// of 4096 (67 MB) take 20.9 us, 16.4 of them here (4.1 TB/s), 4.4 in the join:
+// a workgroup has nine tiles and a wave two or three, which is too few to hide
+// the start (lengths, page numbers, the first K and V, each read waiting for
+// the one before).  One token over 512 tokens: 10.6 us, a chain of such reads.
 #include "kvc_attend_device.hpp"
 
 #include <type_traits>
