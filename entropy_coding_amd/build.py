@@ -17,8 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
 ARCH = os.environ.get("KVC_OFFLOAD_ARCH", "gfx950")
 
-KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip", "kvc_attention_wide.hip"]
-HOST = ["kvc_api.cpp", "kvc_paged_api.cpp"]
+KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip", "kvc_attention_wide.hip",
+           "kvc_qkv.hip"]
+HOST = ["kvc_api.cpp", "kvc_paged_api.cpp", "kvc_step_api.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include "kvc_paged.hpp"
+#include "kvc_round.hpp"
 #include "kvc_wave.hpp"
 
 namespace kvc {
@@ -335,17 +336,6 @@ hipError_t launch_block_table(const TableArgs& args, hipStream_t s) {
 // ---------------------------------------------------------------- append
 
 namespace {
-
-// Two bf16 values (low half first) as the e4m3 of x / scale: the quotient in
-// float32, clamped to +-448 (a NaN passes both comparisons and stays), then
-// rounded to nearest even by the conversion.
-__device__ float clamp448(float x) { return x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x; }
-
-__device__ uint32_t round_pair(uint32_t two, float scale) {
-    const float lo = clamp448(__uint_as_float(two << 16) / scale);
-    const float hi = clamp448(__uint_as_float(two & 0xFFFF0000u) / scale);
-    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, 0, false)) & 0xFFFFu;
-}
 
 // One piece of a row a thread, 16 bytes as it is written, in workgroups of
 // 256 pieces; blockIdx.y: K or V.  A prompt of 16384 rows of 1024 bf16 values

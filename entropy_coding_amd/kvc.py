@@ -37,6 +37,7 @@ EXPORTS = [
     "kvc_build_marginal", "kvc_estimate_bits", "kvc_cdf_table",
     "kvc_build_block_table", "kvc_block_table_result", "kvc_paged_append",
     "kvc_paged_attention_sizes", "kvc_paged_attention", "kvc_paged_attention_result",
+    "kvc_paged_qkv",
 ]
 
 if not os.path.exists(LIB_PATH):
@@ -93,6 +94,20 @@ class kvc_attention(ctypes.Structure):
         ("max_tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("channels", ctypes.c_int64),
         ("kv_dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float), ("k_scale", ctypes.c_float),
         ("v_scale", ctypes.c_float),
+    ]
+
+
+class kvc_qkv(ctypes.Structure):
+    _fields_ = [
+        ("d_q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("d_k", ctypes.c_void_p), ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("d_v", ctypes.c_void_p), ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("d_q_out", ctypes.c_void_p), ("q_out_row_stride", ctypes.c_int64),
+        ("d_q_norm", ctypes.c_void_p), ("d_k_norm", ctypes.c_void_p), ("d_frequencies", ctypes.c_void_p),
+        ("d_positions", ctypes.c_void_p), ("d_slots", ctypes.c_void_p),
+        ("rows", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("channels", ctypes.c_int64), ("rotary", ctypes.c_int64),
+        ("kv_dtype", ctypes.c_int32), ("norm_dtype", ctypes.c_int32), ("neighbours", ctypes.c_uint32),
+        ("eps", ctypes.c_float), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
     ]
 
 
@@ -154,6 +169,7 @@ _lib_attention_sizes = _sig("kvc_paged_attention_sizes", ctypes.c_int,
 _lib_attention = _sig("kvc_paged_attention", ctypes.c_int,
                       [ctypes.POINTER(kvc_paged_kv), _I64, ctypes.POINTER(kvc_attention), _P, _U64, _P])
 _lib_attention_result = _sig("kvc_paged_attention_result", ctypes.c_int, [_P, _P])
+_lib_qkv = _sig("kvc_paged_qkv", ctypes.c_int, [ctypes.POINTER(kvc_paged_kv), _I64, ctypes.POINTER(kvc_qkv), _P])
 
 
 class KvcError(RuntimeError):
@@ -656,6 +672,97 @@ def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tenso
                                       rows, k.stride(0), v.stride(0), slots.data_ptr(), k_scale, v_scale, s),
                 k, v, slots, *(paged.pools if stream is not None else ()), own=(paged._own,))
     _check(st, "kvc_paged_append")
+
+
+def _qkv_rows(t, name, shape, device):
+    """A projection's rows [rows, heads, channels] (None: any number of rows),
+    bf16, views of wider rows allowed."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3 or (shape[0] is not None and t.shape[0] != shape[0]) \
+            or t.shape[1:] != shape[1:] or (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{name} must be bf16 [{'rows' if shape[0] is None else shape[0]}, {shape[1]}, {shape[2]}] on "
+                         f"{device}, channels contiguous")
+
+
+class PagedQKV:
+    """Norms of queries and keys, rotation by position and the append of keys
+    and values to the pages, in one pass over a projection's rows.  q_norm and
+    k_norm [layers, channels] (bf16 or float32, both of one type; None: no
+    norm); frequencies [rotary / 2] float64, radians a position (None: no
+    rotation), pairing channels i and rotary / 2 + i, or 2 i and 2 i + 1 with
+    interleaved.  Threads need an object each; calls on several streams do not."""
+
+    def __init__(self, paged: PagedKV, q_heads: int, frequencies: torch.Tensor | None = None,
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0):
+        paged._check_pools()
+        self.paged, self.q_heads, self.device = paged, q_heads, paged.block_table.device
+        ch, layers = paged.channels, paged.desc.n_pools // 2
+        norms = [t for t in (q_norm, k_norm) if t is not None]
+        dtype = norms[0].dtype if norms else torch.bfloat16
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("norms must be bf16 or float32")
+        for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None:
+                _tensor(t, name, dtype, (layers, ch), self.device)
+                if t.data_ptr() % 16:
+                    raise ValueError(f"{name} must be 16-byte aligned")
+        if frequencies is not None:
+            _tensor(frequencies, "frequencies", torch.float64, (None,), self.device)
+            if frequencies.shape[0] % 8 or not 0 < 2 * frequencies.shape[0] <= ch:
+                raise ValueError(f"frequencies must be a multiple of 8, at most {ch // 2}")
+        if norms and not (math.isfinite(eps) and eps >= 1e-30):
+            raise ValueError("eps must be at least 1e-30")
+        if not 0 <= q_heads <= 65536 or ch > 256:
+            raise ValueError("q_heads must be 0 to 65536, channels at most 256")
+        for x in (k_scale, v_scale):
+            if not (math.isfinite(x) and x > 0) or (paged.kv_dtype == KVC_BF16 and x != 1.0):
+                raise ValueError("scales must be finite and positive, and 1 for bf16 pools")
+        self._norms = q_norm, k_norm
+        home = torch._C._cuda_getCurrentRawStream(self.device.index)
+        self._own = (paged._own, *((home, t) for t in (*norms, frequencies) if t is not None))
+        self._layer_bytes = ch * dtype.itemsize
+        self.desc = kvc_qkv(q_heads=q_heads, channels=ch, kv_dtype=paged.kv_dtype,
+                            rotary=0 if frequencies is None else 2 * frequencies.shape[0], d_frequencies=_ptr(frequencies),
+                            norm_dtype=KVC_F32 if dtype == torch.float32 else KVC_BF16, neighbours=int(interleaved), eps=eps,
+                            k_scale=k_scale, v_scale=v_scale)
+        self._ref = ctypes.byref(self.desc)
+
+    def __call__(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                 positions: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Queue the rows q [rows, q_heads, channels], k and v [rows, heads,
+        channels] (bf16, views allowed) of one layer: keys and values to slots
+        [rows] (int64; -1: none), queries to out, which may be q (returned;
+        rows whose position, int32 [rows], is negative keep what it holds)."""
+        d, dev, paged = self.desc, self.device, self.paged
+        ch, heads = paged.channels, paged.desc.heads
+        rows = k.shape[0]
+        _qkv_rows(q, "q", (rows, self.q_heads, ch), dev)
+        _qkv_rows(k, "k", (None, heads, ch), dev)
+        _qkv_rows(v, "v", (rows, heads, ch), dev)
+        _tensor(slots, "slots", torch.int64, (rows,), dev)
+        if positions is not None:
+            _tensor(positions, "positions", torch.int32, (rows,), dev)
+        elif d.rotary:
+            raise ValueError("a rotation needs positions")
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty((rows, self.q_heads, ch), dtype=q.dtype, device=dev)
+        if out is not q:
+            _qkv_rows(out, "out", (rows, self.q_heads, ch), dev)
+        if not _rows_contiguous(out):
+            raise ValueError("out's heads must lie one after the other")
+        d.rows = rows
+        d.d_q, d.q_row_stride, d.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+        d.d_k, d.k_row_stride, d.k_head_stride = k.data_ptr(), k.stride(0), k.stride(1)
+        d.d_v, d.v_row_stride, d.v_head_stride = v.data_ptr(), v.stride(0), v.stride(1)
+        d.d_q_out, d.q_out_row_stride = out.data_ptr(), out.stride(0)
+        d.d_slots, d.d_positions = slots.data_ptr(), _ptr(positions)
+        norms = [None if t is None else t.data_ptr() + layer * self._layer_bytes for t in self._norms]
+        d.d_q_norm, d.d_k_norm = norms
+        st = _queue(dev, stream, lambda s: _lib_qkv(paged.ref, layer, self._ref, s), q, k, v, slots, positions, out,
+                    *(paged.pools if stream is not None else ()), own=self._own)
+        _check(st, "kvc_paged_qkv")
+        return out
 
 
 class PagedAttention:

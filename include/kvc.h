@@ -531,6 +531,66 @@ int kvc_paged_attention(const kvc_paged_kv* h_paged, int64_t layer, const kvc_at
 int kvc_paged_attention_result(const void* d_workspace, void* stream);
 
 /*
+ * Queries, keys and values of a layer's new tokens on their way from the
+ * projection: norms, rotation by position, and the append, in one pass.  Row
+ * r of d_q, d_k and d_v is one token; q_heads heads of queries and h_paged's
+ * heads of keys and values, of `channels` bf16 values each.  For a head x of
+ * the queries (d_q_norm given) or keys (d_k_norm)
+ *     y = x / sqrt(mean(x^2) + eps) * norm,
+ * with one weight a channel, the same for all heads; without it (NULL) y = x.
+ * Then, with t = d_positions[r] x d_frequencies[i] (radians) for the pair i of
+ * the first `rotary` channels, channels i and rotary / 2 + i, or with
+ * neighbours = 1 channels 2 i and 2 i + 1:
+ *     (a, b) -> (a cos t - b sin t, a sin t + b cos t).
+ * Queries are rounded to bf16 into d_q_out (which may be d_q, with the same
+ * strides).  Keys and values go to slot d_slots[r] of pools 2 x layer and 2 x
+ * layer + 1: keys rounded to the pools' type once, values as kvc_paged_append
+ * writes them (bf16 bit for bit; e4m3 of the float32 quotients x / k_scale and
+ * x / v_scale, to nearest even, saturated at +-448, NaN kept; scales finite
+ * and positive, 1 for bf16 pools).  Of a row whose position is negative
+ * nothing is written; of one whose slot is negative or past the pools no key
+ * and value.  Two rows of one slot leave a mix of both.  A sum of squares is
+ * float32, and float64 where that would overflow; t is formed in float64 and
+ * whole turns are taken off there, so that every position has the same
+ * precision; all else is float32.
+ * channels 64, 128, 192 or 256; rotary a multiple of 16 from 0 (no rotation:
+ * d_frequencies and d_positions may be NULL) to channels; eps at least 1e-30
+ * where there is a norm; q_heads 0 (d_q and d_q_out not looked at) to 65536.
+ * d_q, d_k, d_v, d_q_out, the norms and the pools 16-byte aligned.  h_paged's
+ * table is not read and may be NULL.  Does not synchronise; KVC_ERR_INVALID
+ * for bad arguments, nothing launched.
+ */
+typedef struct kvc_qkv {
+    const void* d_q;                /* [rows][q_heads][channels] bf16                 */
+    int64_t q_row_stride;           /* strides in values, multiples of 8 (one between
+                                       one row or one head is not looked at)          */
+    int64_t q_head_stride;
+    const void* d_k;                /* [rows][heads][channels] bf16                   */
+    int64_t k_row_stride;
+    int64_t k_head_stride;
+    const void* d_v;                /* [rows][heads][channels] bf16                   */
+    int64_t v_row_stride;
+    int64_t v_head_stride;
+    void* d_q_out;                  /* [rows][q_heads][channels] bf16                 */
+    int64_t q_out_row_stride;       /* in values, a multiple of 8; heads are channels apart */
+    const void* d_q_norm;           /* [channels] of norm_dtype, or NULL              */
+    const void* d_k_norm;           /* [channels] of norm_dtype, or NULL              */
+    const double* d_frequencies;    /* [rotary / 2] radians a position                */
+    const int32_t* d_positions;     /* [rows]                                         */
+    const int64_t* d_slots;         /* [rows]                                         */
+    int64_t rows;                   /* < 2^31                                         */
+    int64_t q_heads;
+    int64_t channels;
+    int64_t rotary;
+    int32_t kv_dtype;               /* of the pools: KVC_BF16 or KVC_E4M3             */
+    int32_t norm_dtype;             /* KVC_BF16 or KVC_F32                            */
+    uint32_t neighbours;            /* 0 or 1                                         */
+    float eps;
+    float k_scale, v_scale;
+} kvc_qkv;
+int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, void* stream);
+
+/*
  * Sigma calibration ([wiki] "predictor choice": per-(kv, head, channel)
  * variance calibrated on data, then frozen; [blog] "deployment parameters":
  * 128 sequences of 1024 tokens).  d_kv and d_mu are [reps][planes][tokens]

@@ -1,0 +1,67 @@
+"""The host-side checks of the speculative step's calls, with no GPU: bad
+arguments are refused with the status their declarations state before
+anything touches the device (device pointers are stand-in addresses, so the
+module stays off machines with a GPU)."""
+import ctypes
+import math
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from test_host_paged_ops import FAKE, paged_desc
+from test_host_sanitizers import ROOT, _runtime, checked_lib  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(),
+                                reason="stand-in device pointers: host-only checks, kept off GPUs")
+
+
+def qkv_status(kvc, layer=0, **kw):
+    f = dict(d_q=FAKE, q_row_stride=48 * 128, q_head_stride=128, d_k=FAKE, k_row_stride=48 * 128, k_head_stride=128, d_v=FAKE,
+             v_row_stride=48 * 128, v_head_stride=128, d_q_out=FAKE, q_out_row_stride=32 * 128, d_q_norm=FAKE, d_k_norm=FAKE,
+             d_frequencies=FAKE, d_positions=FAKE, d_slots=FAKE, rows=5, q_heads=32, channels=128, rotary=128, kv_dtype=0,
+             norm_dtype=0, neighbours=0, eps=1e-6, k_scale=1.0, v_scale=1.0)
+    f.update({k: v for k, v in kw.items() if k in f})
+    g = paged_desc(kvc, **{k: v for k, v in kw.items() if k not in f})
+    return kvc._lib_qkv(ctypes.byref(g), layer, ctypes.byref(kvc.kvc_qkv(**f)), None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(layer=-1), dict(layer=2), dict(n_pools=3), dict(d_pools=None), dict(num_pages=11), dict(channels=96),
+    dict(channels=320, pool_bytes=1 << 40), dict(channels=0), dict(kv_dtype=2), dict(rows=-1), dict(rows=1 << 31),
+    dict(q_heads=-1), dict(q_heads=65537), dict(neighbours=2), dict(rotary=-16), dict(rotary=144), dict(rotary=8),
+    dict(k_scale=0.0), dict(v_scale=math.nan), dict(k_scale=0.5), dict(kv_dtype=1, v_scale=-1.0), dict(norm_dtype=1),
+    dict(norm_dtype=3), dict(d_q_norm=FAKE + 8), dict(d_k_norm=FAKE + 2), dict(eps=0.0), dict(eps=math.nan), dict(eps=math.inf),
+    dict(eps=-1e-6), dict(eps=1e-31), dict(d_q_norm=None, eps=0.0), dict(d_frequencies=None), dict(d_frequencies=FAKE + 4),
+    dict(d_positions=None), dict(d_positions=FAKE + 2), dict(d_q=None), dict(d_q=FAKE + 8), dict(d_k=None), dict(d_k=FAKE + 2),
+    dict(d_v=None), dict(d_v=FAKE + 8), dict(d_slots=None), dict(d_slots=FAKE + 4), dict(d_q_out=None), dict(d_q_out=FAKE + 8),
+    dict(q_row_stride=4), dict(q_row_stride=-8), dict(q_head_stride=12), dict(k_row_stride=-8), dict(k_head_stride=4),
+    dict(v_row_stride=1 << 41), dict(v_head_stride=2), dict(q_out_row_stride=32 * 128 - 8), dict(q_out_row_stride=32 * 128 + 4),
+    dict(reserved=1),
+])
+def test_qkv_refuses(kvc, bad):
+    assert qkv_status(kvc, **bad) == kvc.KVC_ERR_INVALID
+
+
+def test_qkv_of_no_rows_launches_nothing(kvc):
+    assert qkv_status(kvc, rows=0, d_q=None, d_k=None, d_v=None, d_slots=None, d_q_out=None) == kvc.KVC_OK
+    assert kvc._lib_qkv(ctypes.byref(paged_desc(kvc)), 0, None, None) == kvc.KVC_ERR_INVALID
+
+
+def test_step_host_logic_under_the_sanitizers(checked_lib):  # noqa: F811
+    """This module's refusals against the library whose host code is built
+    with AddressSanitizer and UndefinedBehaviorSanitizer."""
+    if os.environ.get("KVC_LIBRARY"):
+        pytest.skip("already running on the sanitizer build")
+    env = dict(os.environ)
+    env["KVC_LIBRARY"] = checked_lib
+    env["LD_PRELOAD"] = ":".join(p for p in [_runtime("libasan.so"), env.get("LD_PRELOAD", "")] if p)
+    env["ASAN_OPTIONS"] = "detect_leaks=0:abort_on_error=1:halt_on_error=1"
+    env["UBSAN_OPTIONS"] = "halt_on_error=1:print_stacktrace=1"
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider",
+                        "tests/test_host_step_ops.py", "-k", "not sanitizers"],
+                       cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "passed" in r.stdout, (r.stdout + r.stderr)[-4000:]
+    assert "ERROR: AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-4000:]
