@@ -1,6 +1,6 @@
 // Host-side interface between the C ABI (kvc_step_api.cpp) and the kernels of
 // a speculative step around the attention over pages: norms, rotation and
-// append (kvc_qkv.hip).
+// append (kvc_qkv.hip), verification of drafted tokens (kvc_verify.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -31,5 +31,68 @@ struct QkvArgs {
     float eps, k_scale, v_scale;
 };
 hipError_t launch_qkv(const QkvArgs& args, int64_t channels, bool fp8, bool neighbours, hipStream_t s);
+
+// ---- verification
+
+constexpr int kMaxNodes = 1024;         // of a sequence's tree
+constexpr int kMaxVocab = 1 << 20;
+constexpr int kVerifyChunk = 4096;      // values of a distribution that a workgroup sums
+
+// Head of the workspace; behind it two words a sequence (what the walk and
+// the draw found wrong), a VerifyState each, the tokens rejected at the node
+// where a sequence stops and the scales between its rejections, by row, and
+// the chunks' sums.
+struct VerifyControl {
+    uint32_t magic;
+    uint32_t batch;
+};
+struct VerifyState {                    // where a sequence stops
+    int32_t start, rows;                // rows 0: nothing to draw
+    int32_t stop;                       // row of the node
+    int32_t last;                       // row of the drawn token in out_tokens
+    int32_t rejected;                   // entries of its lists
+    int32_t pad[3];
+};
+struct VerifySums {                     // units of 2^-42
+    uint64_t left, whole;               // after the rejections, and before
+};
+struct VerifyLayout {
+    uint64_t words, states, rejects, scales, sums, total;
+    uint32_t chunks;
+};
+inline VerifyLayout verify_layout(int64_t batch, int64_t rows, int64_t vocab) {
+    const auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
+    VerifyLayout l;
+    l.chunks = static_cast<uint32_t>((vocab + kVerifyChunk - 1) / kVerifyChunk);
+    l.words = 256;
+    l.states = l.words + up(8 * uint64_t(batch));
+    l.rejects = l.states + up(sizeof(VerifyState) * uint64_t(batch));
+    l.scales = l.rejects + up(4 * uint64_t(rows));
+    l.sums = l.scales + up(4 * uint64_t(rows));
+    l.total = l.sums + up(sizeof(VerifySums) * uint64_t(batch) * l.chunks);
+    return l;
+}
+struct VerifyArgs {
+    int64_t batch, rows;
+    uint32_t vocab, chunks;
+    const int32_t* row_starts;
+    const int32_t* tokens;
+    const int32_t* parents;             // null: chains
+    const float* target;
+    const float* draft;                 // null: drafted without probabilities
+    int64_t target_row, draft_row;
+    const float* accept;
+    const float* sample;
+    int32_t* kept;
+    int32_t* kept_lens;
+    int32_t* out_tokens;
+    VerifyControl* ctl;
+    uint32_t* words;
+    VerifyState* states;
+    int32_t* rejects;
+    float* scales;
+    VerifySums* sums;
+};
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 
 }  // namespace kvc

@@ -15,8 +15,21 @@ namespace {
 using kvc::aligned;
 using kvc::kInt31;
 using kvc::kMaxScalars;
+using kvc::outcome;
 using kvc::pools_ok;
 using kvc::positive;
+using kvc::read_back;
+
+// The flags that a call left for its sequences, `words` of them.
+int outcome_of_words(const void* d_words, uint64_t words, hipStream_t s) {
+    uint32_t flags = 0, part[1024];
+    for (uint64_t at = 0; at < words; at += 1024) {
+        const uint64_t n = words - at < 1024 ? words - at : 1024;
+        if (!read_back(part, static_cast<const uint32_t*>(d_words) + at, 4 * n, s)) return KVC_ERR_DEVICE;
+        for (uint64_t i = 0; i < n; ++i) flags |= part[i];
+    }
+    return outcome(flags);
+}
 
 // Rows of a projection; a stride between one row or one head is not looked at.
 bool heads_ok(const void* d, int64_t row_stride, int64_t head_stride, int64_t rows, int64_t heads) {
@@ -26,6 +39,12 @@ bool heads_ok(const void* d, int64_t row_stride, int64_t head_stride, int64_t ro
 
 kvc::HeadRows head_rows(const void* d, int64_t row_stride, int64_t head_stride, int64_t rows, int64_t heads) {
     return kvc::HeadRows{static_cast<const uint16_t*>(d), rows > 1 ? row_stride : 0, heads > 1 ? head_stride : 0};
+}
+
+bool verify_sizes_ok(const kvc_drafts* p) {
+    if (!p || p->batch < 1 || p->batch > 1 << 20 || p->rows < 0 || p->rows >= kInt31) return false;
+    if (p->vocab < 1 || p->vocab > kvc::kMaxVocab) return false;
+    return p->batch * ((p->vocab + kvc::kVerifyChunk - 1) / kvc::kVerifyChunk) < 1 << 24;   // workgroups of a launch
 }
 
 }  // namespace
@@ -80,6 +99,62 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
     a.v_scale = p->v_scale;
     return kvc::launch_qkv(a, p->channels, p->kv_dtype == KVC_E4M3, p->neighbours != 0,
                            static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
+}
+
+int kvc_verify_drafts_sizes(const kvc_drafts* p, uint64_t* h_workspace_bytes) {
+    if (!h_workspace_bytes || !verify_sizes_ok(p)) return KVC_ERR_INVALID;
+    *h_workspace_bytes = kvc::verify_layout(p->batch, p->rows, p->vocab).total;
+    return KVC_OK;
+}
+
+int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace_bytes, void* stream) {
+    if (!verify_sizes_ok(p) || !d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    const auto stride_ok = [p](int64_t s) { return p->rows < 2 || (s >= p->vocab && s <= kMaxScalars); };
+    if (!p->d_row_starts || !p->d_kept_lens || !p->d_sample) return KVC_ERR_INVALID;
+    if (p->rows > 0 && (!p->d_tokens || !p->d_target || !p->d_accept || !p->d_kept || !p->d_out_tokens)) return KVC_ERR_INVALID;
+    for (const void* d : {static_cast<const void*>(p->d_row_starts), static_cast<const void*>(p->d_tokens),
+                          static_cast<const void*>(p->d_parents), static_cast<const void*>(p->d_target),
+                          static_cast<const void*>(p->d_draft), static_cast<const void*>(p->d_accept),
+                          static_cast<const void*>(p->d_sample), static_cast<const void*>(p->d_kept),
+                          static_cast<const void*>(p->d_kept_lens), static_cast<const void*>(p->d_out_tokens)})
+        if (!aligned(d, 4)) return KVC_ERR_INVALID;
+    if (!stride_ok(p->target_row_stride) || (p->d_draft && !stride_ok(p->draft_row_stride))) return KVC_ERR_INVALID;
+    const kvc::VerifyLayout l = kvc::verify_layout(p->batch, p->rows, p->vocab);
+    if (workspace_bytes < l.total) return KVC_ERR_CAPACITY;
+    char* const ws = static_cast<char*>(d_workspace);
+    kvc::VerifyArgs a;
+    a.batch = p->batch;
+    a.rows = p->rows;
+    a.vocab = static_cast<uint32_t>(p->vocab);
+    a.chunks = l.chunks;
+    a.row_starts = p->d_row_starts;
+    a.tokens = p->d_tokens;
+    a.parents = p->d_parents;
+    a.target = p->d_target;
+    a.draft = p->d_draft;
+    a.target_row = p->target_row_stride;
+    a.draft_row = p->draft_row_stride;
+    a.accept = p->d_accept;
+    a.sample = p->d_sample;
+    a.kept = p->d_kept;
+    a.kept_lens = p->d_kept_lens;
+    a.out_tokens = p->d_out_tokens;
+    a.ctl = static_cast<kvc::VerifyControl*>(d_workspace);
+    a.words = reinterpret_cast<uint32_t*>(ws + l.words);
+    a.states = reinterpret_cast<kvc::VerifyState*>(ws + l.states);
+    a.rejects = reinterpret_cast<int32_t*>(ws + l.rejects);
+    a.scales = reinterpret_cast<float*>(ws + l.scales);
+    a.sums = reinterpret_cast<kvc::VerifySums*>(ws + l.sums);
+    return kvc::launch_verify(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
+}
+
+int kvc_verify_drafts_result(const void* d_workspace, void* stream) {
+    if (!d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    kvc::VerifyControl c;
+    if (!read_back(&c, d_workspace, sizeof(c), s)) return KVC_ERR_DEVICE;
+    if (c.magic != kvc::kPagedMagic) return KVC_ERR_INVALID;
+    return outcome_of_words(static_cast<const char*>(d_workspace) + 256, 2 * uint64_t(c.batch), s);
 }
 
 }  // extern "C"

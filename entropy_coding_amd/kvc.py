@@ -37,7 +37,7 @@ EXPORTS = [
     "kvc_build_marginal", "kvc_estimate_bits", "kvc_cdf_table",
     "kvc_build_block_table", "kvc_block_table_result", "kvc_paged_append",
     "kvc_paged_attention_sizes", "kvc_paged_attention", "kvc_paged_attention_result",
-    "kvc_paged_qkv",
+    "kvc_paged_qkv", "kvc_verify_drafts_sizes", "kvc_verify_drafts", "kvc_verify_drafts_result",
 ]
 
 if not os.path.exists(LIB_PATH):
@@ -111,6 +111,16 @@ class kvc_qkv(ctypes.Structure):
     ]
 
 
+class kvc_drafts(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+        ("d_row_starts", ctypes.c_void_p), ("d_tokens", ctypes.c_void_p), ("d_parents", ctypes.c_void_p),
+        ("d_target", ctypes.c_void_p), ("target_row_stride", ctypes.c_int64), ("d_draft", ctypes.c_void_p),
+        ("draft_row_stride", ctypes.c_int64), ("d_accept", ctypes.c_void_p), ("d_sample", ctypes.c_void_p),
+        ("d_kept", ctypes.c_void_p), ("d_kept_lens", ctypes.c_void_p), ("d_out_tokens", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _U64 = ctypes.c_uint64
 _I64 = ctypes.c_int64
@@ -170,6 +180,9 @@ _lib_attention = _sig("kvc_paged_attention", ctypes.c_int,
                       [ctypes.POINTER(kvc_paged_kv), _I64, ctypes.POINTER(kvc_attention), _P, _U64, _P])
 _lib_attention_result = _sig("kvc_paged_attention_result", ctypes.c_int, [_P, _P])
 _lib_qkv = _sig("kvc_paged_qkv", ctypes.c_int, [ctypes.POINTER(kvc_paged_kv), _I64, ctypes.POINTER(kvc_qkv), _P])
+_lib_verify_sizes = _sig("kvc_verify_drafts_sizes", ctypes.c_int, [ctypes.POINTER(kvc_drafts), ctypes.POINTER(_U64)])
+_lib_verify = _sig("kvc_verify_drafts", ctypes.c_int, [ctypes.POINTER(kvc_drafts), _P, _U64, _P])
+_lib_verify_result = _sig("kvc_verify_drafts_result", ctypes.c_int, [_P, _P])
 
 
 class KvcError(RuntimeError):
@@ -849,6 +862,79 @@ def kvc_paged_attention(paged: PagedKV, layer: int, q: torch.Tensor, row_starts:
     got = att(layer, q, row_starts, context_lens, tree_mask, stream=stream)
     att.result(stream)
     return got
+
+
+class DraftVerifier:
+    """Verification of drafted tokens of `batch` sequences, up to max_rows
+    nodes a call: holds the workspace, so that repeated calls allocate nothing
+    where their outputs are given.  Calls that may run at the same time need
+    an object each."""
+
+    def __init__(self, batch: int, vocab: int, max_rows: int, device="cuda"):
+        self.batch, self.vocab, self.max_rows = batch, vocab, max_rows
+        self.desc = kvc_drafts(batch=batch, rows=max_rows, vocab=vocab)
+        self._ref = ctypes.byref(self.desc)
+        n = _U64(0)
+        _check(_lib_verify_sizes(self._ref, ctypes.byref(n)), "kvc_verify_drafts_sizes")
+        self.device = torch.empty(0, device=device).device
+        self._own = _workspace(n.value, self.device)
+        self.workspace = self._own[1]
+
+    def _rows_of(self, t, name, rows):
+        if t.dtype != torch.float32 or t.device != self.device or t.shape != (rows, self.vocab) or \
+                (self.vocab > 1 and rows and t.stride(1) != 1):
+            raise ValueError(f"{name} must be float32 [{rows}, {self.vocab}] on {self.device}, a row's values contiguous")
+
+    def __call__(self, target: torch.Tensor, tokens: torch.Tensor, row_starts: torch.Tensor, accept: torch.Tensor,
+                 sample: torch.Tensor, parents: torch.Tensor | None = None, draft: torch.Tensor | None = None,
+                 kept: torch.Tensor | None = None, kept_lens: torch.Tensor | None = None,
+                 out_tokens: torch.Tensor | None = None, stream=None):
+        """Queue the verification of the nodes tokens [rows] (int32; of each
+        sequence the first is its last token) of trees given by parents [rows]
+        (int32, places in the sequence; None: chains) against the
+        probabilities target [rows, vocab] behind each of them, draft those
+        that its children were drawn from (float32; None: picked without);
+        accept [rows] and sample [batch] float32 random numbers in [0, 1).
+        Returns (kept [rows], kept_lens [batch], out_tokens [rows]), int32:
+        the kept nodes' places, their number, the new tokens (-1 behind).
+        result() gives the outcome."""
+        d, dev = self.desc, self.device
+        rows = tokens.shape[0]
+        if rows > self.max_rows:
+            raise ValueError(f"at most {self.max_rows} rows")
+        _tensor(tokens, "tokens", torch.int32, (rows,), dev)
+        _tensor(row_starts, "row_starts", torch.int32, (self.batch + 1,), dev)
+        _tensor(accept, "accept", torch.float32, (rows,), dev)
+        _tensor(sample, "sample", torch.float32, (self.batch,), dev)
+        if parents is not None:
+            _tensor(parents, "parents", torch.int32, (rows,), dev)
+        self._rows_of(target, "target", rows)
+        if draft is not None:
+            self._rows_of(draft, "draft", rows)
+        if kept is None or kept_lens is None or out_tokens is None:
+            with torch.cuda.stream(stream):
+                make = lambda n, t: torch.empty(n, dtype=torch.int32, device=dev) if t is None else t
+                kept, kept_lens, out_tokens = make(rows, kept), make(self.batch, kept_lens), make(rows, out_tokens)
+        _tensor(kept, "kept", torch.int32, (rows,), dev)
+        _tensor(kept_lens, "kept_lens", torch.int32, (self.batch,), dev)
+        _tensor(out_tokens, "out_tokens", torch.int32, (rows,), dev)
+        d.rows = rows
+        d.d_row_starts, d.d_tokens, d.d_parents = row_starts.data_ptr(), tokens.data_ptr(), _ptr(parents)
+        d.d_target, d.target_row_stride = target.data_ptr(), target.stride(0)
+        d.d_draft, d.draft_row_stride = _ptr(draft), 0 if draft is None else draft.stride(0)
+        d.d_accept, d.d_sample = accept.data_ptr(), sample.data_ptr()
+        d.d_kept, d.d_kept_lens, d.d_out_tokens = kept.data_ptr(), kept_lens.data_ptr(), out_tokens.data_ptr()
+        ws = self.workspace
+        st = _queue(dev, stream, lambda s: _lib_verify(self._ref, ws.data_ptr(), ws.numel(), s), target, tokens, row_starts,
+                    accept, sample, parents, draft, kept, kept_lens, out_tokens, own=(self._own,))
+        _check(st, "kvc_verify_drafts")
+        return kept, kept_lens, out_tokens
+
+    def result(self, stream=None) -> None:
+        """Waits for the last call; raises KvcError if it met trees, tokens or
+        probabilities that do not fit."""
+        st = _queue(self.device, stream, lambda s: _lib_verify_result(self.workspace.data_ptr(), s))
+        _check(st, "kvc_verify_drafts")
 
 
 def calibrate_workspace_bytes(planes: int, channels: int) -> int:

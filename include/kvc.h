@@ -591,6 +591,78 @@ typedef struct kvc_qkv {
 int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, void* stream);
 
 /*
+ * Verification of drafted tokens against the target's probabilities, with
+ * given random numbers: what is kept is distributed as if the target had been
+ * sampled token by token.  Sequence b's n_b = d_row_starts[b + 1] -
+ * d_row_starts[b] rows (at most KVC_MAX_DRAFT_NODES) are the nodes of a tree:
+ * node 0 the last token that the sequence has (its d_tokens entry is not
+ * looked at), node i > 0 a drafted token behind node d_parents[row] < i (a
+ * place in the sequence, not a row; d_parents NULL: i - 1, a chain).  Row r of
+ * d_target holds the target's probabilities of the token behind node r, row r
+ * of d_draft (where given) those that the children of node r were drawn from,
+ * each child by itself.  Beginning with node 0, the children of the current
+ * node are tested in the order of their rows; with y the target's row at
+ * first, t a child's token and u its d_accept entry:
+ *   - with d_draft (q its row), after a rejection y is first scaled by the
+ *     float32 of 1 / sum(y); the child is accepted where u q[t] < y[t]; else y
+ *     becomes max(y - q, 0);
+ *   - without (tokens picked, not drawn) it is accepted where u m < y[t], m
+ *     being 1 less the y[t] of the children rejected before; else y[t]
+ *     becomes 0.
+ * An accepted child becomes the current node, with a new y.  Where no child is
+ * accepted the walk stops and the last token is drawn from y (from the
+ * target's row where sum(y) is 0): the first x whose sum(y[0 .. x]) is greater
+ * than floor(u S), u being d_sample[b] and S the whole sum.
+ * Out come d_kept_lens[b], the nodes kept, node 0 among them (1 to n_b; 0
+ * where n_b is 0); d_kept[row starts + j], the j-th of them; and d_out_tokens
+ * [row starts + j], the sequence's new tokens, one a kept node, the drawn one
+ * last; both -1 behind.  Rows behind d_row_starts[batch] are left as they
+ * were.
+ * Probabilities are float32 and compared in float64 (u m of large m rounded
+ * to it); y is float32, each step rounded once; sums count whole units of
+ * 2^-42, rounded down, and are exact: nothing depends on an order of
+ * summation.  What is no number from 0 to 1 counts as the nearer of them, NaN
+ * as 0; rows of probabilities are taken to sum to 1.  Random numbers lie in
+ * [0, 1).
+ * vocab and batch at most 2^20, batch x ceil(vocab / 4096) < 2^24; a row
+ * stride (in values, at least vocab) between one row is not looked at.  Does not synchronise.
+ * kvc_verify_drafts_result gives KVC_ERR_INVALID where a sequence's row starts
+ * fall or pass `rows` or it has too many nodes (its kept length is then 0 and
+ * nothing else of it written), where a parent does not come before its node
+ * (which is then not reached), a token lies outside the vocabulary (it is
+ * never accepted), or the probabilities that a token is drawn from are all 0
+ * (the token is then -1).
+ * Workspace: kvc_verify_drafts_sizes (of batch, rows and vocab), 256-byte
+ * aligned.
+ */
+#define KVC_MAX_DRAFT_NODES 1024
+typedef struct kvc_drafts {
+    int64_t batch;
+    int64_t rows;                   /* < 2^31                                         */
+    int64_t vocab;
+    const int32_t* d_row_starts;    /* [batch + 1]                                    */
+    const int32_t* d_tokens;        /* [rows]                                         */
+    const int32_t* d_parents;       /* [rows] or NULL                                 */
+    const float* d_target;          /* [rows][vocab]                                  */
+    int64_t target_row_stride;
+    const float* d_draft;           /* [rows][vocab] or NULL                          */
+    int64_t draft_row_stride;
+    const float* d_accept;          /* [rows]                                         */
+    const float* d_sample;          /* [batch]                                        */
+    int32_t* d_kept;                /* [rows]                                         */
+    int32_t* d_kept_lens;           /* [batch]                                        */
+    int32_t* d_out_tokens;          /* [rows]                                         */
+} kvc_drafts;
+int kvc_verify_drafts_sizes(const kvc_drafts* p, uint64_t* h_workspace_bytes);
+int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * Outcome of the last kvc_verify_drafts queued with this workspace:
+ * synchronises `stream` and returns its status.
+ */
+int kvc_verify_drafts_result(const void* d_workspace, void* stream);
+
+/*
  * Sigma calibration ([wiki] "predictor choice": per-(kv, head, channel)
  * variance calibrated on data, then frozen; [blog] "deployment parameters":
  * 128 sequences of 1024 tokens).  d_kv and d_mu are [reps][planes][tokens]

@@ -52,3 +52,59 @@ def tolerance_e4m3(z, size):
     """z: the quotient by the scale; size likewise."""
     e = size * FLOAT_ERROR + np.abs(z) * 2.0 ** -24
     return np.maximum(E4M3_HALF * (np.abs(z) + e), E4M3_LEAST) + e
+
+
+# ---------------------------------------------------------------- verification
+
+UNIT = 2.0 ** 42
+
+
+def clean(p):
+    """Probabilities as they count: float32 in [0, 1], NaN as 0."""
+    return np.clip(np.where(np.isnan(p), np.float32(0), p), np.float32(0), np.float32(1)).astype(np.float32)
+
+
+def units(y):
+    return np.floor(y.astype(np.float64) * UNIT).astype(np.int64)
+
+
+def verify(starts, tokens, parents, target, draft, accept, sample):
+    """Per sequence (kept places, new tokens), walked node by node."""
+    out = []
+    for b in range(len(starts) - 1):
+        s, n = int(starts[b]), int(starts[b + 1] - starts[b])
+        if n <= 0 or s < 0 or s + n > len(tokens) or n > 1024:
+            out.append(([], []))
+            continue
+        path, y, rejected, mass = [0], clean(target[s]), 0, 1 << 42
+        for i in range(1, n):
+            if (i - 1 if parents is None else parents[s + i]) != path[-1]:
+                continue
+            t, u = int(tokens[s + i]), np.float64(accept[s + i])
+            there = 0 <= t < len(y)
+            if draft is not None:
+                q = clean(draft[s + path[-1]])
+                if rejected:
+                    z = int(units(y).sum())
+                    y = y * (np.float32(UNIT / np.float64(z)) if z else np.float32(0))
+                ok = there and u * np.float64(q[t]) < np.float64(y[t])
+                if not ok:
+                    y = np.maximum(y - q, np.float32(0))
+            else:
+                ok = there and u * np.float64(mass) < np.float64(y[t]) * UNIT
+                if not ok and there:
+                    mass = max(0, mass - int(units(y[t])))
+                    y = y.copy()
+                    y[t] = 0
+            rejected += 1
+            if ok:
+                path, y, rejected, mass = path + [i], clean(target[s + i]), 0, 1 << 42
+        if units(y).sum() == 0:
+            y = clean(target[s + path[-1]])
+        upto = np.cumsum(units(y))
+        total = int(upto[-1])
+        u = float(sample[b])
+        point = min(int(u * float(total)) if u > 0 else 0, total - 1)
+        last = int((upto <= point).sum()) if total else -1
+        out.append((path, [int(tokens[s + i]) for i in path[1:]] + [last]))
+    return out

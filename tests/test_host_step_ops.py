@@ -50,6 +50,49 @@ def test_qkv_of_no_rows_launches_nothing(kvc):
     assert kvc._lib_qkv(ctypes.byref(paged_desc(kvc)), 0, None, None) == kvc.KVC_ERR_INVALID
 
 
+def verify_status(kvc, ws=FAKE, ws_bytes=1 << 40, sizes=False, **kw):
+    f = dict(batch=3, rows=12, vocab=1000, d_row_starts=FAKE, d_tokens=FAKE, d_parents=FAKE, d_target=FAKE,
+             target_row_stride=1000, d_draft=FAKE, draft_row_stride=1003, d_accept=FAKE, d_sample=FAKE, d_kept=FAKE,
+             d_kept_lens=FAKE, d_out_tokens=FAKE)
+    f.update(kw)
+    p = ctypes.byref(kvc.kvc_drafts(**f))
+    if sizes:
+        n = ctypes.c_uint64(0)
+        return kvc._lib_verify_sizes(p, ctypes.byref(n)), n.value
+    return kvc._lib_verify(p, ws, ws_bytes, None)
+
+
+VERIFY_SIZES_BAD = [dict(batch=0), dict(batch=(1 << 20) + 1), dict(rows=-1), dict(rows=1 << 31), dict(vocab=0),
+                    dict(vocab=(1 << 20) + 1), dict(batch=1 << 16, vocab=1 << 20), dict(batch=1 << 20, vocab=65536)]
+
+
+@pytest.mark.parametrize("bad", VERIFY_SIZES_BAD + [
+    dict(d_row_starts=None), dict(d_tokens=None), dict(d_target=None), dict(d_accept=None), dict(d_sample=None),
+    dict(d_kept=None), dict(d_kept_lens=None), dict(d_out_tokens=None), dict(d_row_starts=FAKE + 2), dict(d_tokens=FAKE + 1),
+    dict(d_parents=FAKE + 2), dict(d_target=FAKE + 2), dict(d_draft=FAKE + 1), dict(d_accept=FAKE + 2), dict(d_sample=FAKE + 3),
+    dict(d_kept=FAKE + 2), dict(d_kept_lens=FAKE + 2), dict(d_out_tokens=FAKE + 2), dict(target_row_stride=999),
+    dict(target_row_stride=1 << 41), dict(draft_row_stride=0), dict(draft_row_stride=-1000), dict(ws=None), dict(ws=FAKE + 128),
+])
+def test_verify_refuses(kvc, bad):
+    assert verify_status(kvc, **bad) == kvc.KVC_ERR_INVALID
+
+
+def test_verify_sizes_and_a_short_workspace(kvc):
+    for bad in VERIFY_SIZES_BAD:
+        assert verify_status(kvc, sizes=True, **bad)[0] == kvc.KVC_ERR_INVALID
+    last = 0
+    for kw in (dict(rows=0), dict(), dict(rows=10 ** 6), dict(rows=10 ** 6, vocab=1 << 20),
+               dict(batch=(1 << 16) - 1, rows=(1 << 31) - 1, vocab=1 << 20)):
+        kw.update(target_row_stride=1 << 20, draft_row_stride=1 << 20)
+        st, n = verify_status(kvc, sizes=True, **kw)
+        assert st == kvc.KVC_OK and n > last
+        last = n
+        assert verify_status(kvc, ws_bytes=n - 1, **kw) == kvc.KVC_ERR_CAPACITY
+    assert kvc._lib_verify(None, FAKE, 1 << 30, None) == kvc.KVC_ERR_INVALID
+    assert kvc._lib_verify_result(None, None) == kvc.KVC_ERR_INVALID
+    assert kvc._lib_verify_result(FAKE + 8, None) == kvc.KVC_ERR_INVALID
+
+
 def test_step_host_logic_under_the_sanitizers(checked_lib):  # noqa: F811
     """This module's refusals against the library whose host code is built
     with AddressSanitizer and UndefinedBehaviorSanitizer."""
