@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libkvc.so")
 ARCH = os.environ.get("KVC_OFFLOAD_ARCH", "gfx950")
 
 KERNELS = ["kvc_kernels.hip", "kvc_paged.hip", "kvc_attention.hip", "kvc_attention_wide.hip",
-           "kvc_qkv.hip", "kvc_verify.hip"]
+           "kvc_qkv.hip", "kvc_verify.hip", "kvc_pages.hip"]
 HOST = ["kvc_api.cpp", "kvc_paged_api.cpp", "kvc_step_api.cpp"]
 
 COMMON = [

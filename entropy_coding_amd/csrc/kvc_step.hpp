@@ -1,6 +1,7 @@
 // Host-side interface between the C ABI (kvc_step_api.cpp) and the kernels of
 // a speculative step around the attention over pages: norms, rotation and
-// append (kvc_qkv.hip), verification of drafted tokens (kvc_verify.hip).
+// append (kvc_qkv.hip), verification of drafted tokens (kvc_verify.hip), rows
+// and pages moved, shared and given back (kvc_pages.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -94,5 +95,73 @@ struct VerifyArgs {
     VerifySums* sums;
 };
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
+
+// ---- pages
+
+struct PagesOf {                        // the pools and the table
+    void* const* pools;
+    int64_t n_pools;
+    int64_t batch, max_pages, num_pages;
+    uint32_t page_tokens;
+    uint32_t pieces;                    // of 16 bytes in a row of a pool
+};
+
+// Head of a compaction's workspace; a word a sequence behind it (at 256).
+struct CompactControl {
+    uint32_t magic;
+    uint32_t batch;
+};
+struct CompactArgs {
+    PagesOf g;
+    const int32_t* table;
+    int64_t rows;
+    const int32_t* row_starts;
+    const int32_t* context;             // null: none has any
+    const int32_t* kept;
+    const int32_t* kept_lens;
+    CompactControl* ctl;
+    uint32_t* words;
+};
+hipError_t launch_compact(const CompactArgs& a, hipStream_t s);
+
+constexpr int kMaxShared = 1024;        // requests of a fork or release
+
+// Head of the workspace of forks and releases (zero before the first); behind
+// it (at 256) a fork's entries, then a bit a page, zero between releases.
+struct SharedControl {
+    uint32_t magic;
+    uint32_t flags;                     // of the last call
+    uint32_t pending;                   // of a release under way, 0 between
+    int32_t entries;                    // of a fork
+};
+struct ForkEntry {
+    int32_t parent, child;
+    int32_t whole, rest;                // the parent's full pages; tokens of its last one
+    int32_t page;                       // the page that these are copied to; -1: none
+    int32_t from;                       // ... and from
+};
+constexpr uint64_t kSharedEntries = 256;
+constexpr uint64_t kSharedBits = kSharedEntries + sizeof(ForkEntry) * kMaxShared;
+static_assert(kSharedBits == 256 + 24 * 1024, "KVC_SHARED_PAGES_WORKSPACE_BYTES");
+struct SharedArgs {
+    PagesOf g;
+    int32_t* table;
+    int64_t free_capacity;
+    const int32_t* held_in;
+    int32_t* held_out;
+    int32_t* free_pages;
+    const int32_t* free_in;
+    int32_t* free_out;
+    int32_t* extra;
+    int32_t count;
+    const int32_t* parents;             // forks
+    const int32_t* children;            // ... or the requests released
+    const int32_t* context;             // forks; null: none has any
+    SharedControl* ctl;
+    ForkEntry* entries;
+    uint32_t* bits;
+};
+hipError_t launch_fork(const SharedArgs& a, hipStream_t s);
+hipError_t launch_release(const SharedArgs& a, hipStream_t s);
 
 }  // namespace kvc

@@ -47,6 +47,59 @@ bool verify_sizes_ok(const kvc_drafts* p) {
     return p->batch * ((p->vocab + kvc::kVerifyChunk - 1) / kvc::kVerifyChunk) < 1 << 24;   // workgroups of a launch
 }
 
+// The pools and the table of a descriptor, for calls that go through all of
+// them.
+bool pages_ok(const kvc_paged_kv* g, int32_t kv_dtype, int64_t channels) {
+    return pools_ok(g, 0, kv_dtype, channels) && g->n_pools <= 1 << 20 && g->batch >= 1 && g->batch < kInt31 &&
+           g->max_pages >= 1 && g->max_pages < kInt31;
+}
+
+kvc::PagesOf pages_of(const kvc_paged_kv* g, int32_t kv_dtype, int64_t channels) {
+    kvc::PagesOf p;
+    p.pools = g->d_pools;
+    p.n_pools = g->n_pools;
+    p.batch = g->batch;
+    p.max_pages = g->max_pages;
+    p.num_pages = g->num_pages;
+    p.page_tokens = g->page_tokens;
+    p.pieces = static_cast<uint32_t>(g->heads * channels * kvc::value_bytes(kv_dtype) / 16);
+    return p;
+}
+
+bool shared_ok(const kvc_paged_kv* g, int32_t kv_dtype, int64_t channels, const kvc_shared_pages* p, int64_t count) {
+    if (!p || !pages_ok(g, kv_dtype, channels) || count < 0 || count > kvc::kMaxShared) return false;
+    if (p->free_capacity < g->num_pages || p->free_capacity >= kInt31) return false;
+    for (const void* d : {static_cast<const void*>(p->d_block_table), static_cast<const void*>(p->d_held_in),
+                          static_cast<const void*>(p->d_held_out), static_cast<const void*>(p->d_free_pages),
+                          static_cast<const void*>(p->d_free_in), static_cast<const void*>(p->d_free_out),
+                          static_cast<const void*>(p->d_extra)})
+        if (!d || !aligned(d, 4)) return false;
+    return true;
+}
+
+kvc::SharedArgs shared_args(const kvc_paged_kv* g, int32_t kv_dtype, int64_t channels, const kvc_shared_pages* p,
+                            int64_t count, void* d_workspace) {
+    char* const ws = static_cast<char*>(d_workspace);
+    kvc::SharedArgs a;
+    a.g = pages_of(g, kv_dtype, channels);
+    a.table = p->d_block_table;
+    a.free_capacity = p->free_capacity;
+    a.held_in = p->d_held_in;
+    a.held_out = p->d_held_out;
+    a.free_pages = p->d_free_pages;
+    a.free_in = p->d_free_in;
+    a.free_out = p->d_free_out;
+    a.extra = p->d_extra;
+    a.count = static_cast<int32_t>(count);
+    a.parents = nullptr;
+    a.children = nullptr;
+    a.context = nullptr;
+    a.ctl = static_cast<kvc::SharedControl*>(d_workspace);
+    a.entries = reinterpret_cast<kvc::ForkEntry*>(ws + kvc::kSharedEntries);
+    a.bits = reinterpret_cast<uint32_t*>(ws + kvc::kSharedBits);
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,6 +208,70 @@ int kvc_verify_drafts_result(const void* d_workspace, void* stream) {
     if (!read_back(&c, d_workspace, sizeof(c), s)) return KVC_ERR_DEVICE;
     if (c.magic != kvc::kPagedMagic) return KVC_ERR_INVALID;
     return outcome_of_words(static_cast<const char*>(d_workspace) + 256, 2 * uint64_t(c.batch), s);
+}
+
+int kvc_paged_compact(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels, int64_t rows,
+                      const int32_t* d_row_starts, const int32_t* d_context_lens, const int32_t* d_kept,
+                      const int32_t* d_kept_lens, void* d_workspace, uint64_t workspace_bytes, void* stream) {
+    if (!pages_ok(h_paged, kv_dtype, channels) || h_paged->batch > 1 << 20 || rows < 0 || rows >= kInt31) return KVC_ERR_INVALID;
+    if (!d_workspace || !aligned(d_workspace, 256) || !h_paged->d_block_table || !aligned(h_paged->d_block_table, 4))
+        return KVC_ERR_INVALID;
+    if (!d_row_starts || !d_kept_lens || (rows > 0 && !d_kept) || !aligned(d_row_starts, 4) || !aligned(d_context_lens, 4) ||
+        !aligned(d_kept, 4) || !aligned(d_kept_lens, 4))
+        return KVC_ERR_INVALID;
+    if (workspace_bytes < KVC_COMPACT_WORKSPACE_BYTES(h_paged->batch)) return KVC_ERR_CAPACITY;
+    kvc::CompactArgs a;
+    a.g = pages_of(h_paged, kv_dtype, channels);
+    a.table = h_paged->d_block_table;
+    a.rows = rows;
+    a.row_starts = d_row_starts;
+    a.context = d_context_lens;
+    a.kept = d_kept;
+    a.kept_lens = d_kept_lens;
+    a.ctl = static_cast<kvc::CompactControl*>(d_workspace);
+    a.words = reinterpret_cast<uint32_t*>(static_cast<char*>(d_workspace) + 256);
+    return kvc::launch_compact(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
+}
+
+int kvc_paged_compact_result(const void* d_workspace, void* stream) {
+    if (!d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    kvc::CompactControl c;
+    if (!read_back(&c, d_workspace, sizeof(c), s)) return KVC_ERR_DEVICE;
+    if (c.magic != kvc::kPagedMagic) return KVC_ERR_INVALID;
+    return outcome_of_words(static_cast<const char*>(d_workspace) + 256, c.batch, s);
+}
+
+int kvc_fork_pages(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels, const kvc_shared_pages* p, int64_t count,
+                   const int32_t* d_parents, const int32_t* d_children, const int32_t* d_context_lens, void* d_workspace,
+                   uint64_t workspace_bytes, void* stream) {
+    if (!shared_ok(h_paged, kv_dtype, channels, p, count) || !d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    if ((count > 0 && (!d_parents || !d_children)) || !aligned(d_parents, 4) || !aligned(d_children, 4) ||
+        !aligned(d_context_lens, 4))
+        return KVC_ERR_INVALID;
+    if (workspace_bytes < KVC_SHARED_PAGES_WORKSPACE_BYTES(h_paged->num_pages)) return KVC_ERR_CAPACITY;
+    kvc::SharedArgs a = shared_args(h_paged, kv_dtype, channels, p, count, d_workspace);
+    a.parents = d_parents;
+    a.children = d_children;
+    a.context = d_context_lens;
+    return kvc::launch_fork(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
+}
+
+int kvc_release_pages(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels, const kvc_shared_pages* p,
+                      int64_t count, const int32_t* d_requests, void* d_workspace, uint64_t workspace_bytes, void* stream) {
+    if (!shared_ok(h_paged, kv_dtype, channels, p, count) || !d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    if ((count > 0 && !d_requests) || !aligned(d_requests, 4)) return KVC_ERR_INVALID;
+    if (workspace_bytes < KVC_SHARED_PAGES_WORKSPACE_BYTES(h_paged->num_pages)) return KVC_ERR_CAPACITY;
+    kvc::SharedArgs a = shared_args(h_paged, kv_dtype, channels, p, count, d_workspace);
+    a.children = d_requests;
+    return kvc::launch_release(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
+}
+
+int kvc_shared_pages_result(const void* d_workspace, void* stream) {
+    if (!d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
+    kvc::SharedControl c;
+    if (!read_back(&c, d_workspace, sizeof(c), static_cast<hipStream_t>(stream))) return KVC_ERR_DEVICE;
+    return c.magic == kvc::kPagedMagic ? outcome(c.flags) : KVC_ERR_INVALID;
 }
 
 }  // extern "C"

@@ -38,6 +38,7 @@ EXPORTS = [
     "kvc_build_block_table", "kvc_block_table_result", "kvc_paged_append",
     "kvc_paged_attention_sizes", "kvc_paged_attention", "kvc_paged_attention_result",
     "kvc_paged_qkv", "kvc_verify_drafts_sizes", "kvc_verify_drafts", "kvc_verify_drafts_result",
+    "kvc_paged_compact", "kvc_paged_compact_result", "kvc_fork_pages", "kvc_release_pages", "kvc_shared_pages_result",
 ]
 
 if not os.path.exists(LIB_PATH):
@@ -121,6 +122,14 @@ class kvc_drafts(ctypes.Structure):
     ]
 
 
+class kvc_shared_pages(ctypes.Structure):
+    _fields_ = [
+        ("free_capacity", ctypes.c_int64), ("d_block_table", ctypes.c_void_p), ("d_held_in", ctypes.c_void_p),
+        ("d_held_out", ctypes.c_void_p), ("d_free_pages", ctypes.c_void_p), ("d_free_in", ctypes.c_void_p),
+        ("d_free_out", ctypes.c_void_p), ("d_extra", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _U64 = ctypes.c_uint64
 _I64 = ctypes.c_int64
@@ -183,6 +192,13 @@ _lib_qkv = _sig("kvc_paged_qkv", ctypes.c_int, [ctypes.POINTER(kvc_paged_kv), _I
 _lib_verify_sizes = _sig("kvc_verify_drafts_sizes", ctypes.c_int, [ctypes.POINTER(kvc_drafts), ctypes.POINTER(_U64)])
 _lib_verify = _sig("kvc_verify_drafts", ctypes.c_int, [ctypes.POINTER(kvc_drafts), _P, _U64, _P])
 _lib_verify_result = _sig("kvc_verify_drafts_result", ctypes.c_int, [_P, _P])
+_lib_compact = _sig("kvc_paged_compact", ctypes.c_int,
+                    [ctypes.POINTER(kvc_paged_kv), _I32, _I64, _I64, _P, _P, _P, _P, _P, _U64, _P])
+_lib_compact_result = _sig("kvc_paged_compact_result", ctypes.c_int, [_P, _P])
+_SHARED_ARGS = [ctypes.POINTER(kvc_paged_kv), _I32, _I64, ctypes.POINTER(kvc_shared_pages), _I64]
+_lib_fork = _sig("kvc_fork_pages", ctypes.c_int, _SHARED_ARGS + [_P, _P, _P, _P, _U64, _P])
+_lib_release = _sig("kvc_release_pages", ctypes.c_int, _SHARED_ARGS + [_P, _P, _U64, _P])
+_lib_shared_result = _sig("kvc_shared_pages_result", ctypes.c_int, [_P, _P])
 
 
 class KvcError(RuntimeError):
@@ -935,6 +951,110 @@ class DraftVerifier:
         probabilities that do not fit."""
         st = _queue(self.device, stream, lambda s: _lib_verify_result(self.workspace.data_ptr(), s))
         _check(st, "kvc_verify_drafts")
+
+
+class PagedCompaction:
+    """Moves the kept ones of a step's drafted tokens together in every pool
+    of a paged cache.  Calls that may run at the same time need an object
+    each."""
+
+    def __init__(self, paged: PagedKV):
+        paged._check_pools()
+        self.paged, self.device, self.batch = paged, paged.block_table.device, paged.desc.batch
+        self._own = _workspace(256 + 4 * self.batch, self.device)
+        self.workspace = self._own[1]
+
+    def __call__(self, row_starts: torch.Tensor, context_lens: torch.Tensor | None, kept: torch.Tensor,
+                 kept_lens: torch.Tensor, stream=None) -> None:
+        """Queue the move: of sequence b's drafted tokens, at positions
+        context_lens[b] and on, the kept_lens[b] tokens kept[row_starts[b] + j]
+        (places that rise) go to context_lens[b] + j; row_starts [batch + 1],
+        context_lens and kept_lens [batch], kept [rows], all int32.  result()
+        gives the outcome."""
+        dev, paged = self.device, self.paged
+        _tensor(row_starts, "row_starts", torch.int32, (self.batch + 1,), dev)
+        _tensor(kept, "kept", torch.int32, (None,), dev)
+        _tensor(kept_lens, "kept_lens", torch.int32, (self.batch,), dev)
+        if context_lens is not None:
+            _tensor(context_lens, "context_lens", torch.int32, (self.batch,), dev)
+        ws = self.workspace
+        st = _queue(dev, stream,
+                    lambda s: _lib_compact(paged.ref, paged.kv_dtype, paged.channels, kept.shape[0], row_starts.data_ptr(),
+                                           _ptr(context_lens), kept.data_ptr(), kept_lens.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), s),
+                    row_starts, context_lens, kept, kept_lens, paged.block_table,
+                    *(paged.pools if stream is not None else ()), own=(self._own, paged._own))
+        _check(st, "kvc_paged_compact")
+
+    def result(self, stream=None) -> None:
+        """Waits for the last call; raises KvcError if it met lengths, places
+        or page numbers that do not fit."""
+        st = _queue(self.device, stream, lambda s: _lib_compact_result(self.workspace.data_ptr(), s))
+        _check(st, "kvc_paged_compact")
+
+
+class SharedPages:
+    """Requests that start from another's tokens and share its full pages.
+    The state is BlockTable's (the table of `paged`, held [batch], free_pages,
+    free_count [1]) and a count of each page's further holders, extra
+    [num_pages] (0 for pages that one request holds, or none), all int32 and
+    the caller's; a call updates them in place, or writes held_out and
+    free_count_out where they are given.  A request whose pages were shared
+    ends with release(), not with a trim.  Calls that may run at the same time
+    need an object each."""
+
+    def __init__(self, paged: PagedKV, held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                 extra: torch.Tensor, held_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None):
+        paged._check_pools()
+        self.paged, self.device = paged, paged.block_table.device
+        self.held, self.free_pages, self.free_count, self.extra = held, free_pages, free_count, extra
+        self.held_out = held if held_out is None else held_out
+        self.free_count_out = free_count if free_count_out is None else free_count_out
+        batch, num_pages = paged.desc.batch, paged.desc.num_pages
+        for t, name, n in ((held, "held", batch), (self.held_out, "held_out", batch), (free_pages, "free_pages", None),
+                           (free_count, "free_count", 1), (self.free_count_out, "free_count_out", 1),
+                           (extra, "extra", num_pages)):
+            _tensor(t, name, torch.int32, (n,), self.device)
+        if free_pages.shape[0] < num_pages:
+            raise ValueError(f"free_pages must have room for {num_pages} pages")
+        self._own = _workspace(256 + 24 * 1024 + 4 * ((num_pages + 31) // 32), self.device)
+        self.workspace = self._own[1]
+        self.desc = kvc_shared_pages(free_pages.numel(), _ptr(paged.block_table), _ptr(held), _ptr(self.held_out),
+                                     _ptr(free_pages), _ptr(free_count), _ptr(self.free_count_out), _ptr(extra))
+        self._ref = ctypes.byref(self.desc)
+
+    def _run(self, call, where, count, stream, *tensors):
+        paged, ws = self.paged, self.workspace
+        args = [_ptr(t) for t in tensors]
+        st = _queue(self.device, stream,
+                    lambda s: call(paged.ref, paged.kv_dtype, paged.channels, self._ref, count, *args, ws.data_ptr(),
+                                   ws.numel(), s),
+                    *tensors, self.held, self.held_out, self.free_pages, self.free_count, self.free_count_out, self.extra,
+                    paged.block_table, *(paged.pools if stream is not None else ()), own=(self._own, paged._own))
+        _check(st, where)
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, context_lens: torch.Tensor | None, stream=None) -> None:
+        """Queue the fork: request children[k], which holds no page, gets the
+        context_lens[parents[k]] tokens of request parents[k] (int32, up to
+        1024; a child of -1: none); context_lens int32 [batch].  result()
+        gives the outcome."""
+        _tensor(children, "children", torch.int32, (None,), self.device)
+        _tensor(parents, "parents", torch.int32, (children.shape[0],), self.device)
+        if context_lens is not None:
+            _tensor(context_lens, "context_lens", torch.int32, (self.paged.desc.batch,), self.device)
+        self._run(_lib_fork, "kvc_fork_pages", children.shape[0], stream, parents, children, context_lens)
+
+    def release(self, requests: torch.Tensor, stream=None) -> None:
+        """Queue the release of the requests (int32, up to 1024; -1: none):
+        pages that nobody else holds go to the stack.  result() gives the
+        outcome."""
+        _tensor(requests, "requests", torch.int32, (None,), self.device)
+        self._run(_lib_release, "kvc_release_pages", requests.shape[0], stream, requests)
+
+    def result(self, stream=None) -> None:
+        """Waits for the last call; raises KvcError if it failed."""
+        st = _queue(self.device, stream, lambda s: _lib_shared_result(self.workspace.data_ptr(), s))
+        _check(st, "kvc_shared_pages")
 
 
 def calibrate_workspace_bytes(planes: int, channels: int) -> int:

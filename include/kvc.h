@@ -663,6 +663,108 @@ int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace
 int kvc_verify_drafts_result(const void* d_workspace, void* stream);
 
 /*
+ * Kept tokens moved together.  Of sequence b's drafted tokens (as
+ * kvc_paged_attention sees them: n_b rows, token i at position
+ * d_context_lens[b] + i) the d_kept_lens[b] tokens d_kept[d_row_starts[b] + j],
+ * places that rise with j, stay: in every pool of h_paged, the row of the
+ * j-th goes to position d_context_lens[b] + j.  What kvc_verify_drafts gives
+ * is taken as it is; the sequence's context is then d_context_lens[b] +
+ * d_kept_lens[b], and kvc_build_block_table with trim gives the rest back.
+ * Rows of other positions are left as they were (those behind the last kept
+ * one hold what they held, or a kept row's copy).  A drafted token's page must
+ * not stand in another request's row of the table.
+ * d_context_lens NULL: none has any.  batch at most 2^20, at most 2^20 pools,
+ * which are 16-byte aligned.  Does not synchronise.  kvc_paged_compact_result
+ * gives KVC_ERR_INVALID where a sequence's row starts fall or pass `rows`, its
+ * lengths are negative or pass its row of the table or 2^31 tokens, more is
+ * kept than there is, or places do not rise or lie outside its rows (nothing
+ * of it is moved), or where a page number lies outside [0, num_pages) (the
+ * rows that it concerns are not moved).
+ * Workspace: KVC_COMPACT_WORKSPACE_BYTES(batch), 256-byte aligned.
+ */
+#define KVC_COMPACT_WORKSPACE_BYTES(batch) (256u + 4u * (uint64_t)(batch))
+int kvc_paged_compact(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels, int64_t rows,
+                      const int32_t* d_row_starts, const int32_t* d_context_lens, const int32_t* d_kept,
+                      const int32_t* d_kept_lens, void* d_workspace, uint64_t workspace_bytes,
+                      void* stream);
+
+/*
+ * Outcome of the last kvc_paged_compact queued with this workspace:
+ * synchronises `stream` and returns its status.
+ */
+int kvc_paged_compact_result(const void* d_workspace, void* stream);
+
+/*
+ * Requests that start from another's tokens: pages held by several requests,
+ * with a count of the further holders of every page (d_extra[page], 0 where
+ * one request holds it or none; pages that kvc_build_block_table hands out
+ * have 0).  The state is that of kvc_build_block_table: the table, the pages
+ * each request holds, the stack of free pages.  With P = page_tokens:
+ *
+ * kvc_fork_pages: for k < count, request c = d_children[k], which holds
+ * no page, gets the T = d_context_lens[p] tokens of request p =
+ * d_parents[k] (NULL: none has any):
+ *   - the first T / P pages of p's row of the table are entered in c's, and
+ *     d_extra of each goes up by one;
+ *   - where P does not divide T, a page is popped from the stack (children in
+ *     their order) and entered behind them, and the T % P tokens of p's
+ *     next page are copied to it in every pool of h_paged;
+ *   - c holds ceil(T / P) pages.
+ * A child of -1 is none (padding); no request may be a child twice.  The child
+ * can then be extended like any request: its new tokens' pages are its own.
+ * All or nothing: on KVC_ERR_INVALID (a request outside the batch, a child
+ * that holds pages, is its parent or stands twice, a parent that holds fewer
+ * pages than its tokens need or more than max_pages, a negative length,
+ * *d_free_in outside [0, free_capacity], a page to be popped or copied from
+ * outside [0, num_pages)) and KVC_ERR_CAPACITY (fewer pages free than wanted)
+ * the held counts and the height of the stack are what they were and nothing
+ * else is written.  A page number outside the pools among those entered in a
+ * child's row is KVC_ERR_INVALID too: it is entered, not counted.
+ *
+ * kvc_release_pages: the requests d_requests[k], k < count (-1: none), are
+ * finished: each page that they hold loses a holder (d_extra goes down by
+ * one); pages that had no further holder go to the stack, in ascending order,
+ * the highest on top; their d_extra is 0; the requests hold none.
+ * KVC_ERR_INVALID for a request outside the batch, a held count outside [0,
+ * max_pages] (both left alone), a request that stands twice (released once),
+ * a page number outside the pools (passed over), a page that loses more
+ * holders than it has (given back once), or a *d_free_in outside [0,
+ * free_capacity] (nothing is done); KVC_ERR_CAPACITY where the stack would
+ * pass free_capacity (pages of several entries of it: what fits is pushed).
+ *
+ * A request whose pages were shared is finished with kvc_release_pages, not
+ * with a trim, and not trimmed below the tokens that it was forked from or
+ * with.  d_held_out / d_free_out may be d_held_in / d_free_in, or other
+ * arrays.  count at most 1024, at most 2^20 pools, which are 16-byte aligned;
+ * free_capacity at least num_pages.  Neither call synchronises;
+ * kvc_shared_pages_result gives the outcome of the last one of either kind
+ * queued with the workspace.
+ * Workspace: KVC_SHARED_PAGES_WORKSPACE_BYTES(num_pages), 256-byte aligned,
+ * all zero before the first call that uses it.
+ */
+#define KVC_MAX_SHARED_REQUESTS 1024
+#define KVC_SHARED_PAGES_WORKSPACE_BYTES(num_pages) \
+    (256u + 24u * 1024u + 4u * (((uint64_t)(num_pages) + 31u) / 32u))
+typedef struct kvc_shared_pages {
+    int64_t free_capacity;          /* entries of d_free_pages, < 2^31                */
+    int32_t* d_block_table;         /* [batch][max_pages] of h_paged                  */
+    const int32_t* d_held_in;       /* [batch]                                        */
+    int32_t* d_held_out;            /* [batch]                                        */
+    int32_t* d_free_pages;          /* [free_capacity]                                */
+    const int32_t* d_free_in;       /* [1]                                            */
+    int32_t* d_free_out;            /* [1]                                            */
+    int32_t* d_extra;               /* [num_pages]                                    */
+} kvc_shared_pages;
+int kvc_fork_pages(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels,
+                   const kvc_shared_pages* p, int64_t count, const int32_t* d_parents,
+                   const int32_t* d_children, const int32_t* d_context_lens, void* d_workspace,
+                   uint64_t workspace_bytes, void* stream);
+int kvc_release_pages(const kvc_paged_kv* h_paged, int32_t kv_dtype, int64_t channels,
+                      const kvc_shared_pages* p, int64_t count, const int32_t* d_requests,
+                      void* d_workspace, uint64_t workspace_bytes, void* stream);
+int kvc_shared_pages_result(const void* d_workspace, void* stream);
+
+/*
  * Sigma calibration ([wiki] "predictor choice": per-(kv, head, channel)
  * variance calibrated on data, then frozen; [blog] "deployment parameters":
  * 128 sequences of 1024 tokens).  d_kv and d_mu are [reps][planes][tokens]

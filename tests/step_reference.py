@@ -108,3 +108,52 @@ def verify(starts, tokens, parents, target, draft, accept, sample):
         last = int((upto <= point).sum()) if total else -1
         out.append((path, [int(tokens[s + i]) for i in path[1:]] + [last]))
     return out
+
+
+# ---------------------------------------------------------------- pages
+
+def compact(pools, table, page, starts, contexts, kept, lens):
+    """pools [n, pages, page, ...] on the host, in place."""
+    for b in range(len(lens)):
+        for j in range(int(lens[b])):
+            x, y = int(contexts[b] + kept[starts[b] + j]), int(contexts[b] + j)
+            if x != y:
+                pools[:, table[b, y // page], y % page] = pools[:, table[b, x // page], x % page]
+
+
+def fork(pools, table, held, free, count, extra, page, parents, children, lens):
+    """On copies (pools in place): (table, held, count, extra)."""
+    table, held, extra = table.copy(), held.copy(), extra.copy()
+    for p, c in zip(parents, children):
+        if c == -1:
+            continue
+        whole, rest = divmod(int(lens[p]), page)
+        table[c, :whole] = table[p, :whole]
+        for j in range(whole):
+            extra[table[p, j]] += 1
+        if rest:
+            count -= 1
+            table[c, whole] = free[count]
+            pools[:, free[count], :rest] = pools[:, table[p, whole], :rest]
+        held[c] = whole + (rest > 0)
+    return table, held, count, extra
+
+
+def release(table, held, free, count, extra, requests):
+    """On copies: (held, free, count, extra)."""
+    held, free, extra = held.copy(), free.copy(), extra.copy()
+    gone = []
+    for r in requests:
+        if r == -1:
+            continue
+        for j in range(held[r]):
+            page = table[r, j]
+            if extra[page] == 0:
+                gone.append(page)
+            else:
+                extra[page] -= 1
+        held[r] = 0
+    for page in sorted(gone):
+        free[count] = page
+        count += 1
+    return held, free, count, extra

@@ -93,6 +93,66 @@ def test_verify_sizes_and_a_short_workspace(kvc):
     assert kvc._lib_verify_result(FAKE + 8, None) == kvc.KVC_ERR_INVALID
 
 
+def compact_status(kvc, ws=FAKE, ws_bytes=256 + 12, kv_dtype=0, ch=128, rows=12, starts=FAKE, context=FAKE, kept=FAKE,
+                   lens=FAKE, **kw):
+    return kvc._lib_compact(ctypes.byref(paged_desc(kvc, **kw)), kv_dtype, ch, rows, starts, context, kept, lens, ws, ws_bytes,
+                            None)
+
+
+PAGES_BAD = [dict(n_pools=3), dict(n_pools=0), dict(n_pools=(1 << 20) + 2), dict(kv_dtype=2), dict(ch=0), dict(ch=96),
+             dict(heads=0), dict(num_pages=0), dict(num_pages=11), dict(page_tokens=0), dict(d_pools=None), dict(d_pools=FAKE + 4),
+             dict(reserved=1), dict(batch=0), dict(max_pages=0), dict(max_pages=1 << 31), dict(ws=None), dict(ws=FAKE + 64)]
+
+
+@pytest.mark.parametrize("bad", PAGES_BAD + [
+    dict(batch=(1 << 20) + 1), dict(rows=-1), dict(rows=1 << 31), dict(starts=None), dict(kept=None), dict(lens=None),
+    dict(starts=FAKE + 2), dict(context=FAKE + 2), dict(kept=FAKE + 1), dict(lens=FAKE + 2), dict(d_block_table=None),
+    dict(d_block_table=FAKE + 2),
+])
+def test_compact_refuses(kvc, bad):
+    assert compact_status(kvc, **bad) == kvc.KVC_ERR_INVALID
+
+
+def test_compact_refuses_a_short_workspace(kvc):
+    assert compact_status(kvc, ws_bytes=256 + 11) == kvc.KVC_ERR_CAPACITY
+    assert kvc._lib_compact_result(None, None) == kvc.KVC_ERR_INVALID
+    assert kvc._lib_compact_result(FAKE + 8, None) == kvc.KVC_ERR_INVALID
+
+
+def shared_status(kvc, fork, ws=FAKE, ws_bytes=256 + 24 * 1024 + 4, kv_dtype=0, ch=128, count=3, parents=FAKE, children=FAKE,
+                  context=FAKE, **kw):
+    f = dict(free_capacity=10, d_table=FAKE, d_held_in=FAKE, d_held_out=FAKE, d_free_pages=FAKE, d_free_in=FAKE,
+             d_free_out=FAKE, d_extra=FAKE)
+    f.update({k: v for k, v in kw.items() if k in f})
+    f["d_block_table"] = f.pop("d_table")
+    g = ctypes.byref(paged_desc(kvc, **{k: v for k, v in kw.items() if k not in f and k != "d_table"}))
+    p = ctypes.byref(kvc.kvc_shared_pages(**f))
+    if fork:
+        return kvc._lib_fork(g, kv_dtype, ch, p, count, parents, children, context, ws, ws_bytes, None)
+    return kvc._lib_release(g, kv_dtype, ch, p, count, children, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("fork", [True, False])
+@pytest.mark.parametrize("bad", PAGES_BAD + [
+    dict(count=-1), dict(count=1025), dict(children=None), dict(children=FAKE + 2), dict(free_capacity=9),
+    dict(free_capacity=1 << 31), dict(d_table=None), dict(d_held_in=None), dict(d_held_out=None), dict(d_free_pages=None),
+    dict(d_free_in=None), dict(d_free_out=None), dict(d_extra=None), dict(d_table=FAKE + 2), dict(d_held_in=FAKE + 1),
+    dict(d_held_out=FAKE + 2), dict(d_free_pages=FAKE + 2), dict(d_free_in=FAKE + 2), dict(d_free_out=FAKE + 2),
+    dict(d_extra=FAKE + 3),
+])
+def test_shared_pages_refuse(kvc, fork, bad):
+    assert shared_status(kvc, fork, **bad) == kvc.KVC_ERR_INVALID
+
+
+def test_forks_refuse(kvc):
+    for bad in (dict(parents=None), dict(parents=FAKE + 2), dict(context=FAKE + 2)):
+        assert shared_status(kvc, True, **bad) == kvc.KVC_ERR_INVALID
+    for fork in (True, False):
+        assert shared_status(kvc, fork, ws_bytes=256 + 24 * 1024 + 3) == kvc.KVC_ERR_CAPACITY
+    assert kvc._lib_shared_result(None, None) == kvc.KVC_ERR_INVALID
+    assert kvc._lib_shared_result(FAKE + 128, None) == kvc.KVC_ERR_INVALID
+
+
 def test_step_host_logic_under_the_sanitizers(checked_lib):  # noqa: F811
     """This module's refusals against the library whose host code is built
     with AddressSanitizer and UndefinedBehaviorSanitizer."""
