@@ -195,7 +195,7 @@ int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace
     a.ctl = static_cast<kvc::VerifyControl*>(d_workspace);
     a.words = reinterpret_cast<uint32_t*>(ws + l.words);
     a.states = reinterpret_cast<kvc::VerifyState*>(ws + l.states);
-    a.rejects = reinterpret_cast<int32_t*>(ws + l.rejects);
+    a.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
     a.scales = reinterpret_cast<float*>(ws + l.scales);
     a.sums = reinterpret_cast<kvc::VerifySums*>(ws + l.sums);
     return kvc::launch_verify(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;

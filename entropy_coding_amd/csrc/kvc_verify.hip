@@ -57,23 +57,19 @@ __device__ void load4(const float* row, uint32_t at, uint32_t vocab, float (&x)[
     }
 }
 
-// The sum over a workgroup, in every thread; a thread's halves are of at most
-// VALUES values.  (A value is at most 1, up to what the scale after a
-// rejection is off by where next to nothing was left; together they are less
-// than 2 each, so that 1024 of them pass no 32 bits.)
-template <int THREADS, int VALUES>
+// The sum over a workgroup, in every thread.  A thread's halves are of at most
+// 1024 values: a value is at most 1, up to what the scale after a rejection is
+// off by where next to nothing was left; together they are less than 2 each,
+// so that 1024 of them pass no 32 bits, and a wave's threads are summed by
+// halves.
+template <int THREADS>
 __device__ uint64_t block_sum(Units x, uint64_t* of_wave) {
-    uint64_t all;
-    if (VALUES * 64 <= 1024) {
-        all = Units{of_lane(scan(x.high), 63), of_lane(scan(x.low), 63)}.all();
-    } else {
-        const uint32_t parts[3] = {x.high >> 16, x.high & 0xFFFFu, x.low >> 16};
-        uint32_t sum[3];
+    const uint32_t parts[3] = {x.high >> 16, x.high & 0xFFFFu, x.low >> 16};
+    uint32_t halves[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) sum[i] = of_lane(scan(parts[i]), 63);
-        all = ((uint64_t(sum[0]) << 16) + sum[1]) << 21;
-        all += (uint64_t(sum[2]) << 16) + of_lane(scan(x.low & 0xFFFFu), 63);
-    }
+    for (int i = 0; i < 3; ++i) halves[i] = of_lane(scan(parts[i]), 63);
+    uint64_t all = ((uint64_t(halves[0]) << 16) + halves[1]) << 21;
+    all += (uint64_t(halves[2]) << 16) + of_lane(scan(x.low & 0xFFFFu), 63);
     if ((threadIdx.x & 63) == 63) of_wave[threadIdx.x >> 6] = all;
     __syncthreads();
     uint64_t sum = 0;
@@ -85,265 +81,425 @@ __device__ uint64_t block_sum(Units x, uint64_t* of_wave) {
 
 // ---- the walk
 
-struct Nodes {
-    int32_t parent[kMaxNodes];                  // -1: of none that can be reached
-    int32_t token[kMaxNodes];                   // -1: none of the vocabulary
-    float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];
-    int32_t path[kMaxNodes];
+// One sequence's tree.
+struct Tree {
+    int64_t start;
+    int n;                                      // 0: nothing to walk
+    bool bad;
+};
+__device__ Tree tree_of(const VerifyArgs& a, int64_t b) {
+    const int64_t start = a.row_starts[b], end = a.row_starts[b + 1];
+    Tree t;
+    t.bad = start < 0 || end < start || end > a.rows || end - start > kMaxNodes;
+    t.start = start;
+    t.n = t.bad ? 0 : static_cast<int>(end - start);
+    return t;
+}
+
+// Node i as a lane has it.
+struct Node {
+    int parent, token;                          // -1: none that can be reached, none of the vocabulary
+    float u, p, q;
+    bool wrong;
+};
+__device__ Node node_of(const VerifyArgs& a, const Tree& t, int i) {
+    Node x{-1, -1, 0.0f, 0.0f, 0.0f, false};
+    if (i < 1 || i >= t.n) return x;            // (of the first nothing is looked at)
+    const int64_t r = t.start + i;
+    const int parent = a.parents ? a.parents[r] : i - 1, token = a.tokens[r];
+    x.u = a.accept[r];
+    if (parent >= 0 && parent < i) x.parent = parent;
+    else x.wrong = true;
+    if (token >= 0 && token < static_cast<int64_t>(a.vocab)) x.token = token;
+    else x.wrong = true;
+    if (x.wrong) return x;
+    x.p = clean(a.target[(t.start + parent) * a.target_row + token]);
+    if (a.draft) x.q = clean(a.draft[(t.start + parent) * a.draft_row + token]);
+    return x;
+}
+
+__device__ float value_of_lane(float x, int lane) { return __uint_as_float(of_lane(__float_as_uint(x), lane)); }
+
+// Where a walk is, and what it leaves.
+struct Walk {
+    int32_t path[kMaxNodes], tokens[kMaxNodes]; // kept nodes and theirs
+    int32_t rejects[kMaxNodes];                 // tokens that are out at the current node, each once
+    float scales[kMaxNodes];                    // between its rejections, the second and on
+    int32_t current, kept, rejected, listed;
+    uint32_t wrong;
 };
 
-constexpr int kWalkThreads = 1024;
-
-// A sequence's walk down its tree: nodes are looked at in order, those whose
-// parent is the current node are tested, an accepted one becomes the current
-// one.  Every wave takes it alike, so that all of them meet where a sum over
-// the vocabulary is needed: before a sibling of a rejected node, where nodes
-// were drawn from the draft's probabilities.
-template <int THREADS>
-__global__ __launch_bounds__(THREADS) void k_verify_walk(VerifyArgs a) {
-    __shared__ Nodes nodes;
-    __shared__ float scales[kMaxNodes];
-    __shared__ int32_t rejects[kMaxNodes];
-    __shared__ uint64_t of_wave[THREADS / 64];
-    const int64_t b = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63;
-    if (b == 0 && tid == 0) *a.ctl = VerifyControl{kPagedMagic, static_cast<uint32_t>(a.batch)};
-    const int64_t start = a.row_starts[b], end = a.row_starts[b + 1];
-    const bool bad = start < 0 || end < start || end > a.rows || end - start > kMaxNodes;
-    const int n = bad ? 0 : static_cast<int>(end - start);
-    if (n == 0) {
-        if (tid == 0) {
-            a.kept_lens[b] = 0;
-            a.words[2 * b] = bad ? kPagedInvalid : 0u;
-            a.states[b] = VerifyState{0, 0, 0, 0, 0, {0, 0, 0}};
-        }
-        return;
-    }
-    bool wrong = false;
-    for (int i = tid; i < n; i += THREADS) {
-        const int64_t r = start + i;
-        int parent = a.parents ? a.parents[r] : i - 1;
-        int token = a.tokens[r];
-        if (i > 0 && (parent < 0 || parent >= i)) wrong = true;
-        if (i > 0 && (token < 0 || token >= static_cast<int64_t>(a.vocab))) {
-            wrong = true;
-            token = -1;
-        }
-        if (i == 0 || parent < 0 || parent >= i) parent = -1;
-        const bool there = parent >= 0 && token >= 0;
-        nodes.parent[i] = parent;
-        nodes.token[i] = token;
-        nodes.u[i] = a.accept[r];
-        nodes.p[i] = there ? clean(a.target[(start + parent) * a.target_row + token]) : 0.0f;
-        nodes.q[i] = there && a.draft ? clean(a.draft[(start + parent) * a.draft_row + token]) : 0.0f;
-    }
-    wrong = __syncthreads_or(wrong);
+// The walk down a tree, by whole waves that all take it alike: nodes are
+// looked at in order, 64 at a time in a wave's lanes; those whose parent is
+// the current node are tested, an accepted one becomes the current one.
+// scale(current, rejected) gives what is left after so many rejections its
+// scale, where nodes were drawn from the draft's probabilities and a node has
+// several children; `writes`: whether this thread writes the lists.
+template <class Scale, class Sync>
+__device__ void walk(const VerifyArgs& a, const Tree& t, Walk& w, bool writes, Scale scale, Sync sync) {
+    const int lane = threadIdx.x & 63;
     int current = 0, kept = 1, rejected = 0, listed = 0;
-    uint64_t mass = uint64_t(1) << 42;          // without probabilities: of tokens that were not rejected
-    if (tid == 0) nodes.path[0] = 0;
-    for (int base = 0; base < n; base += 64) {
-        const int i = base + lane;
-        const int parent = i < n ? nodes.parent[i] : -1;
+    uint64_t mass = uint64_t(1) << 42;          // without probabilities: of tokens that are not out
+    bool wrong = false;
+    if (writes) w.path[0] = 0;
+    for (int base = 0; base < t.n; base += 64) {
+        const Node x = node_of(a, t, base + lane);
+        wrong = wrong || x.wrong;
         uint64_t ahead = ~uint64_t(0);          // nodes behind the last one tested
         for (;;) {
-            const uint64_t next = __ballot(parent == current) & ahead;
+            const uint64_t next = __ballot(x.parent == current) & ahead;
             if (!next) break;
-            const int bit = __builtin_ctzll(next), j = base + bit;
+            const int bit = __builtin_ctzll(next);
             ahead = bit == 63 ? 0 : ~uint64_t(0) << (bit + 1);
-            const double u = nodes.u[j];
-            const float p = nodes.p[j], q = nodes.q[j];
-            const int token = nodes.token[j];
+            const double u = value_of_lane(x.u, bit);
+            const float p = value_of_lane(x.p, bit), q = value_of_lane(x.q, bit);
+            const int token = __builtin_amdgcn_readlane(x.token, bit);
             bool ok, again = false;
             if (a.draft) {
-                if (rejected > 0) {
-                    // what the rejections left, over the whole vocabulary
-                    const float* const target = a.target + (start + current) * a.target_row;
-                    const float* const draft = a.draft + (start + current) * a.draft_row;
-                    Units sum{0, 0};
-                    for (uint32_t at = 4 * tid; at < a.vocab; at += 4 * THREADS) {
-                        float x[4], y[4];
-                        load4(target, at, a.vocab, x);
-                        load4(draft, at, a.vocab, y);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum.add(units_of(left_of(x[e], y[e], scales, rejected)));
-                    }
-                    const uint64_t z = block_sum<THREADS, kMaxVocab / THREADS>(sum, of_wave);
-                    if (tid == 0) scales[rejected] = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
-                    __syncthreads();
+                float y = p;
+                if (rejected) {
+                    const float s = scale(current, rejected);
+                    y = left_of(p, q, w.scales, rejected) * s;
                 }
-                float y = left_of(p, q, scales, rejected);
-                if (rejected) y *= scales[rejected];
                 ok = u * double(q) < double(y);
             } else {
-                for (int k = lane; k < listed; k += 64) again = again || rejects[k] == token;
+                for (int k = lane; k < listed; k += 64) again = again || w.rejects[k] == token;
                 again = __any(again);
                 const float y = again ? 0.0f : p;
                 ok = u * static_cast<double>(mass) < double(y) * 0x1p42;
             }
             if (ok) {
-                current = j;
-                if (tid == 0) nodes.path[kept] = j;
+                current = base + bit;
+                if (writes) {
+                    w.path[kept] = current;
+                    w.tokens[kept] = token;
+                }
                 ++kept;
                 rejected = listed = 0;
                 mass = uint64_t(1) << 42;
             } else {
                 ++rejected;
                 if (!a.draft && !again && token >= 0) {
-                    __syncthreads();            // (every wave has read the list)
-                    if (tid == 0) rejects[listed] = token;
-                    __syncthreads();
+                    if (writes) w.rejects[listed] = token;
+                    sync();                     // (the next test reads the list)
                     ++listed;
-                    const uint64_t w = units_of(p).all();
-                    mass = mass > w ? mass - w : 0;
+                    const uint64_t out = units_of(p).all();
+                    mass = mass > out ? mass - out : 0;
                 }
             }
         }
     }
+    const bool any = __any(wrong);
+    if (writes) {
+        w.current = current;
+        w.kept = kept;
+        w.rejected = rejected;
+        w.listed = listed;
+        w.wrong = any ? kPagedInvalid : 0u;
+    }
+}
+
+// What the walk left, for the caller: by a whole workgroup.
+template <int THREADS>
+__device__ void write_walk(const VerifyArgs& a, const Tree& t, const Walk& w, int64_t b) {
+    for (int j = threadIdx.x; j < t.n; j += THREADS) {
+        a.kept[t.start + j] = j < w.kept ? w.path[j] : -1;
+        if (j != w.kept - 1)                    // (there the drawn token goes)
+            a.out_tokens[t.start + j] = j + 1 < w.kept ? w.tokens[j + 1] : -1;
+    }
+    if (threadIdx.x == 0) {
+        a.kept_lens[b] = t.n ? w.kept : 0;
+        a.words[2 * b] = t.n ? w.wrong : t.bad ? kPagedInvalid : 0u;
+    }
+}
+
+constexpr int kWalkThreads = 1024;
+
+// The walk of trees whose nodes were drawn from the draft's probabilities, a
+// workgroup a sequence: before a sibling of a rejected node is tested, all of
+// it sums what the rejections left over the vocabulary.  Bound by the trips to
+// memory of each such sum: a thread has eight loads under way.
+__global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyArgs a) {
+    constexpr int kAtOnce = 4;
+    __shared__ Walk w;
+    __shared__ uint64_t of_wave[kWalkThreads / 64];
+    const int64_t b = blockIdx.x;
+    const int tid = threadIdx.x;
+    const Tree t = tree_of(a, b);
+    const auto scale = [&](int current, int rejected) {
+        const float* const target = a.target + (t.start + current) * a.target_row;
+        const float* const draft = a.draft + (t.start + current) * a.draft_row;
+        Units sum{0, 0};
+        for (uint32_t at = 4 * tid; at < a.vocab; at += 4 * kAtOnce * kWalkThreads) {
+            float x[kAtOnce][4], y[kAtOnce][4];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                load4(target, at + 4 * kWalkThreads * k, a.vocab, x[k]);
+                load4(draft, at + 4 * kWalkThreads * k, a.vocab, y[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum.add(units_of(left_of(x[k][e], y[k][e], w.scales, rejected)));
+        }
+        const uint64_t z = block_sum<kWalkThreads>(sum, of_wave);
+        const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
+        if (tid == 0) w.scales[rejected] = s;
+        __syncthreads();
+        return s;
+    };
+    if (t.n) walk(a, t, w, tid == 0, scale, [] { __syncthreads(); });
     __syncthreads();
-    const int entries = a.draft ? rejected : listed;
-    for (int k = tid; k < entries; k += THREADS) {
-        if (a.draft) a.scales[start + k] = k ? scales[k] : 0.0f;
-        else a.rejects[start + k] = rejects[k];
-    }
-    for (int j = tid; j < n; j += THREADS) {
-        a.kept[start + j] = j < kept ? nodes.path[j] : -1;
-        a.out_tokens[start + j] = j + 1 < kept ? nodes.token[nodes.path[j + 1]] : -1;
-    }
+    write_walk<kWalkThreads>(a, t, w, b);
     if (tid == 0) {
-        a.kept_lens[b] = kept;
-        a.words[2 * b] = wrong ? kPagedInvalid : 0u;
-        a.states[b] = VerifyState{static_cast<int32_t>(start), n, static_cast<int32_t>(start) + current,
-                                  static_cast<int32_t>(start) + kept - 1, entries, {0, 0, 0}};
+        VerifyState s{0, 0, 0, 0, 0, {0, 0, 0}};
+        if (t.n)
+            s = VerifyState{static_cast<int32_t>(t.start), t.n, static_cast<int32_t>(t.start) + w.current,
+                            static_cast<int32_t>(t.start) + w.kept - 1, w.rejected, {0, 0, 0}};
+        a.states[b] = s;
     }
+    if (t.n)
+        for (int k = tid; k < w.rejected; k += kWalkThreads) a.scales[t.start + k] = k ? w.scales[k] : 0.0f;
 }
 
 // ---- the draw
 
-constexpr int kSumThreads = 256;
-constexpr int kGroups = kVerifyChunk / (4 * kSumThreads);
+constexpr int kDrawThreads = 256;
+constexpr int kDrawWaves = kDrawThreads / 64;
+constexpr int kGroups = kVerifyChunk / (4 * kDrawThreads);
+constexpr int kMostChunks = 64;                 // of a workgroup
 
-// The units of a chunk of the distribution that a sequence draws from.
-__global__ __launch_bounds__(kSumThreads) void k_verify_sums(VerifyArgs a) {
-    __shared__ uint64_t of_wave[kSumThreads / 64];
-    const uint32_t b = blockIdx.x / a.chunks, chunk = blockIdx.x - b * a.chunks;
-    const VerifyState s = a.states[b];
-    if (s.rows == 0) return;
-    const float* const target = a.target + s.stop * a.target_row;
-    const float* const draft = a.draft + s.stop * a.draft_row;
-    const float* const scales = a.scales + s.start;
-    const bool both = a.draft && s.rejected > 0;
+// What is left of the values of a chunk that a thread has, and their units
+// before and after the rejections.
+struct Draw {
+    int64_t stop;                               // row of the node
+    int rejected;
+    const float* scales;
+    const int32_t* rejects;
+};
+// The value of a chunk that a thread has as the e-th of its g-th four: fours
+// dealt to the threads in turn (for sums), or all of a thread's one after the
+// other (IN_ORDER).
+template <bool IN_ORDER>
+__device__ uint32_t place_of(uint32_t tid, int g) { return IN_ORDER ? 4 * (kGroups * tid + g) : 4 * (kDrawThreads * g + tid); }
+
+template <bool IN_ORDER>
+__device__ void chunk_of(const VerifyArgs& a, const Draw& d, uint32_t chunk, float (&x)[kGroups][4], float (&left)[kGroups][4]) {
     const uint32_t base = chunk * kVerifyChunk, tid = threadIdx.x;
-    float x[kGroups][4], y[kGroups][4];
+    const float* const target = a.target + d.stop * a.target_row;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) load4(target, base + 4 * (g * kSumThreads + tid), a.vocab, x[g]);
-    Units whole{0, 0}, left{0, 0};
-    if (both) {
+    for (int g = 0; g < kGroups; ++g) load4(target, base + place_of<IN_ORDER>(tid, g), a.vocab, x[g]);
+    if (a.draft && d.rejected > 0) {
+        const float* const draft = a.draft + d.stop * a.draft_row;
+        float q[kGroups][4];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) load4(draft, base + 4 * (g * kSumThreads + tid), a.vocab, y[g]);
+        for (int g = 0; g < kGroups; ++g) load4(draft, base + place_of<IN_ORDER>(tid, g), a.vocab, q[g]);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) left.add(units_of(left_of(x[g][e], y[g][e], scales, s.rejected)));
+            for (int e = 0; e < 4; ++e) left[g][e] = left_of(x[g][e], q[g][e], d.scales, d.rejected);
+        return;
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) whole.add(units_of(x[g][e]));
-    if (!both) {
-        left = whole;
-        // tokens that were rejected are taken out by the thread that has their values
-        for (int k = 0; k < s.rejected; ++k) {
-            const uint32_t token = static_cast<uint32_t>(a.rejects[s.start + k]), at = token - base;
-            if (at >= uint32_t(kVerifyChunk) || (at >> 2) % kSumThreads != tid) continue;
-            const Units w = units_of(clean(target[token]));
-            left.high -= w.high;
-            left.low -= w.low;
-        }
+        for (int e = 0; e < 4; ++e) left[g][e] = x[g][e];
+    if (a.draft) return;
+    for (int k = 0; k < d.rejected; ++k) {      // tokens that are out
+        const uint32_t at = static_cast<uint32_t>(d.rejects[k]) - base;
+        if (at >= uint32_t(kVerifyChunk)) continue;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) left[g][e] = at == place_of<IN_ORDER>(tid, g) + e ? 0.0f : left[g][e];
     }
-    const uint64_t l = block_sum<kSumThreads, 4 * kGroups>(left, of_wave),
-                   w = block_sum<kSumThreads, 4 * kGroups>(whole, of_wave);
-    if (tid == 0) a.sums[blockIdx.x] = VerifySums{l, w};
 }
 
-constexpr int kPickThreads = kVerifyChunk / 4;
+// The sum of the lanes up to this one, of values below 2^62.
+__device__ uint64_t scan_wide(uint64_t x) {
+    constexpr uint32_t kLow = (1u << 21) - 1;
+    const uint32_t low = scan(static_cast<uint32_t>(x) & kLow), mid = scan(static_cast<uint32_t>(x >> 21) & kLow),
+                   high = scan(static_cast<uint32_t>(x >> 42));
+    return (uint64_t(high) << 42) + (uint64_t(mid) << 21) + low;
+}
 
-// The token at which the sum in the vocabulary's order passes the drawn point.
-__global__ __launch_bounds__(kPickThreads) void k_verify_pick(VerifyArgs a) {
-    __shared__ uint64_t of_wave[kPickThreads / 64];
-    const uint32_t b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-    const VerifyState s = a.states[b];
-    if (s.rows == 0) {
-        if (tid == 0) a.words[2 * b + 1] = 0u;
-        return;
+// Chunks of one sequence's distribution, `per` at a time, are summed by a
+// workgroup; the last workgroup of a sequence to be done draws the token.
+// Chains, and trees without probabilities, are walked by every workgroup for
+// itself (WALKS), by its first wave: a chain of trips to memory as long as a
+// kernel of its own would take, and a launch less.
+template <bool WALKS>
+__global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint32_t parts, uint32_t per) {
+    __shared__ Walk w;
+    __shared__ uint64_t of_wave[2][kDrawWaves], of_value[kDrawWaves];
+    __shared__ uint64_t of_chunk[2][kMostChunks][kDrawWaves];
+    __shared__ uint32_t place;
+    __shared__ uint64_t place_before;
+    const uint32_t b = blockIdx.x / parts, part = blockIdx.x - b * parts;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (blockIdx.x == 0 && tid == 0) *a.ctl = VerifyControl{kPagedMagic, static_cast<uint32_t>(a.batch)};
+    const float u = a.sample[b];                // (asked for now: a trip less behind the sums)
+    Draw d;
+    Tree t{};
+    int64_t last;                               // of the sequence's new tokens
+    if (WALKS) {
+        t = tree_of(a, b);
+        if (t.n == 0) {
+            if (part == 0) write_walk<kDrawThreads>(a, t, w, b);
+            if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
+            return;
+        }
+        if (wave == 0)
+            walk(a, t, w, tid == 0, [](int, int) { return 0.0f; }, [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); });
+        __syncthreads();
+        d = Draw{t.start + w.current, a.draft ? w.rejected : w.listed, w.scales, w.rejects};
+        last = t.start + w.kept - 1;
+    } else {
+        const VerifyState s = a.states[b];
+        if (s.rows == 0) {
+            if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
+            return;
+        }
+        d = Draw{s.stop, s.rejected, a.scales + s.start, nullptr};
+        last = s.last;
     }
-    const VerifySums* const sums = a.sums + uint64_t(b) * a.chunks;
-    uint64_t left = 0, whole = 0;
-    for (uint32_t c = 0; c < a.chunks; ++c) {
-        left += sums[c].left;
-        whole += sums[c].whole;
-    }
-    const bool nothing = left == 0;             // the target's own probabilities then
-    const uint64_t total = nothing ? whole : left;
-    if (total == 0) {
-        if (tid == 0) a.words[2 * b + 1] = kPagedInvalid;
-        return;
-    }
-    const float u = a.sample[b];
-    uint64_t point = u > 0.0f ? static_cast<uint64_t>(fmin(double(u), 1.0) * static_cast<double>(total)) : 0;
-    if (point >= total) point = total - 1;
-    uint64_t before = 0;
-    uint32_t chunk = 0;
-    for (; chunk + 1 < a.chunks; ++chunk) {
-        const uint64_t here = nothing ? sums[chunk].whole : sums[chunk].left;
-        if (before + here > point) break;
-        before += here;
-    }
-    const float* const target = a.target + s.stop * a.target_row;
-    const uint32_t at = chunk * kVerifyChunk + 4 * tid;
-    float x[4];
-    load4(target, at, a.vocab, x);
-    if (!nothing && a.draft && s.rejected > 0) {
-        float y[4];
-        load4(a.draft + s.stop * a.draft_row, at, a.vocab, y);
+    float x[kGroups][4], left[kGroups][4];
+    const uint32_t first_chunk = part * per;
+    const uint32_t count = first_chunk + per <= a.chunks ? per : a.chunks - first_chunk;
+    for (uint32_t c = 0; c < count; ++c) {
+        chunk_of<false>(a, d, first_chunk + c, x, left);
+        Units before{0, 0}, after{0, 0};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = left_of(x[e], y[e], a.scales + s.start, s.rejected);
-    } else if (!nothing && !a.draft) {
-        for (int k = 0; k < s.rejected; ++k) {
-            const uint32_t token = static_cast<uint32_t>(a.rejects[s.start + k]);
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = token == at + e ? 0.0f : x[e];
+            for (int e = 0; e < 4; ++e) {
+                before.add(units_of(x[g][e]));
+                after.add(units_of(left[g][e]));
+            }
+        // (a wave's 1024 values pass no 32 bits: see block_sum)
+        const uint64_t sum[2] = {Units{scan(after.high), scan(after.low)}.all(), Units{scan(before.high), scan(before.low)}.all()};
+        if (lane == 63) {
+            of_chunk[0][c][wave] = sum[0];
+            of_chunk[1][c][wave] = sum[1];
         }
     }
-    Units w[4], mine{0, 0};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        w[e] = units_of(x[e]);
-        mine.add(w[e]);
-    }
-    const uint64_t upto = Units{scan(mine.high), scan(mine.low)}.all();     // within the wave
-    if (lane == 63) of_wave[tid >> 6] = upto;
     __syncthreads();
-    uint64_t sum = before + upto - mine.all();
-    for (uint32_t k = 0; k < tid >> 6; ++k) sum += of_wave[k];
-    if (sum <= point && point < sum + mine.all()) {
-        int e = 0;
+    VerifySums* const sums = a.sums + uint64_t(b) * a.chunks;
+    uint64_t mine[2] = {0, 0};
+    if (tid < count) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            sum += w[i].all();
-            if (sum <= point) e = i + 1;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < kDrawWaves; ++k) mine[i] += of_chunk[i][tid][k];
+    }
+    if (parts > 1) {
+        // The sums first, as exchanges: what they return says that they are done where all dies see them, with no
+        // cache to write back (a release and an acquire of every workgroup took four times as long as all the rest).
+        if (wave == 0) {
+            if (lane < count) {
+                VerifySums* const to = sums + first_chunk + lane;
+                const uint64_t done[2] = {
+                    __hip_atomic_exchange(&to->left, mine[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                    __hip_atomic_exchange(&to->whole, mine[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+                asm volatile("" ::"v"(done[0]), "v"(done[1]) : "memory");
+            }
+            if (lane == 0) {
+                place = __hip_atomic_fetch_add(&a.arrived[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (place == parts - 1) __hip_atomic_store(&a.arrived[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
-        a.out_tokens[s.last] = static_cast<int32_t>(at + e);
+        __syncthreads();
+        if (place != parts - 1) return;
+        mine[0] = mine[1] = 0;
+        if (tid < a.chunks) {
+            mine[0] = __hip_atomic_load(&sums[tid].left, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            mine[1] = __hip_atomic_load(&sums[tid].whole, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    // the chunk that the drawn point lies in: a thread a chunk
+    uint64_t upto[2], total[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        upto[i] = scan_wide(mine[i]);
+        if (lane == 63) of_wave[i][wave] = upto[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        total[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kDrawWaves; ++k) {
+            if (k == int(wave)) upto[i] += total[i];
+            total[i] += of_wave[i][k];
+        }
+    }
+    const int which = total[0] == 0;            // nothing is left: the target's own probabilities
+    const uint64_t all = which ? total[1] : total[0];
+    if (all == 0) {
+        if (tid == 0) {
+            a.out_tokens[last] = -1;
+            a.words[2 * b + 1] = kPagedInvalid;
+        }
+        if (WALKS) write_walk<kDrawThreads>(a, t, w, b);
+        return;
+    }
+    uint64_t point = u > 0.0f ? static_cast<uint64_t>(fmin(double(u), 1.0) * static_cast<double>(all)) : 0;
+    if (point >= all) point = all - 1;
+    const uint64_t end = which ? upto[1] : upto[0], first = end - (which ? mine[1] : mine[0]);
+    if (first <= point && point < end) {
+        place = tid;
+        place_before = first;
+    }
+    __syncthreads();
+    // ... and there the value
+    const uint32_t there = place;
+    chunk_of<true>(a, d, there, x, left);
+    Units here{0, 0};
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (which) left[g][e] = x[g][e];
+            here.add(units_of(left[g][e]));
+        }
+    uint64_t sum = Units{scan(here.high), scan(here.low)}.all();
+    if (lane == 63) of_value[wave] = sum;
+    __syncthreads();
+    sum += place_before - here.all();
+#pragma unroll
+    for (int k = 0; k < kDrawWaves - 1; ++k)
+        if (k < int(wave)) sum += of_value[k];
+    if (sum <= point && point < sum + here.all()) {
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * kGroups - 1; ++i) {
+            sum += units_of(left[i / 4][i % 4]).all();
+            if (sum <= point) at = i + 1;
+        }
+        a.out_tokens[last] = static_cast<int32_t>(there * kVerifyChunk + 4 * kGroups * tid + at);
         a.words[2 * b + 1] = 0u;
     }
+    if (WALKS) write_walk<kDrawThreads>(a, t, w, b);
 }
+
+// Workgroups that a call is dealt to, where it has as many chunks.
+constexpr uint32_t kDrawGroups = 1024;
 
 }  // namespace
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
-    if (a.draft && a.parents) k_verify_walk<kWalkThreads><<<static_cast<uint32_t>(a.batch), kWalkThreads, 0, s>>>(a);
-    else k_verify_walk<64><<<static_cast<uint32_t>(a.batch), 64, 0, s>>>(a);
-    k_verify_sums<<<static_cast<uint32_t>(a.batch * a.chunks), kSumThreads, 0, s>>>(a);
-    k_verify_pick<<<static_cast<uint32_t>(a.batch), kPickThreads, 0, s>>>(a);
+    const uint32_t batch = static_cast<uint32_t>(a.batch);
+    uint32_t parts = kDrawGroups / batch;
+    if (parts < (a.chunks + kMostChunks - 1) / kMostChunks) parts = (a.chunks + kMostChunks - 1) / kMostChunks;
+    if (parts > a.chunks) parts = a.chunks;
+    const uint32_t per = (a.chunks + parts - 1) / parts;
+    parts = (a.chunks + per - 1) / per;
+    if (a.draft && a.parents) {
+        k_verify_walk<<<batch, kWalkThreads, 0, s>>>(a);
+        k_verify_draw<false><<<batch * parts, kDrawThreads, 0, s>>>(a, parts, per);
+    } else {
+        k_verify_draw<true><<<batch * parts, kDrawThreads, 0, s>>>(a, parts, per);
+    }
     return hipGetLastError();
 }
 

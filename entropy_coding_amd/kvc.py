@@ -566,6 +566,8 @@ def kvc_decode_paged(stream_bytes, mu, sigma, prefix, paged: PagedKV, workspace,
 
 def _tensor(t, name, dtype, shape, device):
     """A contiguous tensor of this type and shape (None: any extent) on this device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
             or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
@@ -704,12 +706,12 @@ def kvc_paged_append(paged: PagedKV, layer: int, k: torch.Tensor, v: torch.Tenso
 
 
 def _qkv_rows(t, name, shape, device):
-    """A projection's rows [rows, heads, channels] (None: any number of rows),
-    bf16, views of wider rows allowed."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3 or (shape[0] is not None and t.shape[0] != shape[0]) \
-            or t.shape[1:] != shape[1:] or (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{name} must be bf16 [{'rows' if shape[0] is None else shape[0]}, {shape[1]}, {shape[2]}] on "
-                         f"{device}, channels contiguous")
+    """The strides of a projection's rows [rows, heads, channels], bf16, views
+    of wider rows allowed."""
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device or (s[2] != 1 and t.numel()):
+        raise ValueError(f"{name} must be bf16 {list(shape)} on {device}, channels contiguous")
+    return s
 
 
 class PagedQKV:
@@ -746,7 +748,7 @@ class PagedQKV:
         for x in (k_scale, v_scale):
             if not (math.isfinite(x) and x > 0) or (paged.kv_dtype == KVC_BF16 and x != 1.0):
                 raise ValueError("scales must be finite and positive, and 1 for bf16 pools")
-        self._norms = q_norm, k_norm
+        self._norms = _ptr(q_norm), _ptr(k_norm)
         home = torch._C._cuda_getCurrentRawStream(self.device.index)
         self._own = (paged._own, *((home, t) for t in (*norms, frequencies) if t is not None))
         self._layer_bytes = ch * dtype.itemsize
@@ -763,31 +765,32 @@ class PagedQKV:
         [rows] (int64; -1: none), queries to out, which may be q (returned;
         rows whose position, int32 [rows], is negative keep what it holds)."""
         d, dev, paged = self.desc, self.device, self.paged
-        ch, heads = paged.channels, paged.desc.heads
-        rows = k.shape[0]
-        _qkv_rows(q, "q", (rows, self.q_heads, ch), dev)
-        _qkv_rows(k, "k", (None, heads, ch), dev)
-        _qkv_rows(v, "v", (rows, heads, ch), dev)
+        rows = slots.shape[0]
         _tensor(slots, "slots", torch.int64, (rows,), dev)
         if positions is not None:
             _tensor(positions, "positions", torch.int32, (rows,), dev)
+            d.d_positions = positions.data_ptr()
         elif d.rotary:
             raise ValueError("a rotation needs positions")
+        else:
+            d.d_positions = None
+        shape = (rows, self.q_heads, paged.channels)
+        d.q_row_stride, d.q_head_stride, _ = _qkv_rows(q, "q", shape, dev)
         if out is None:
             with torch.cuda.stream(stream):
-                out = torch.empty((rows, self.q_heads, ch), dtype=q.dtype, device=dev)
-        if out is not q:
-            _qkv_rows(out, "out", (rows, self.q_heads, ch), dev)
-        if not _rows_contiguous(out):
+                out = torch.empty(shape, dtype=q.dtype, device=dev)
+        d.q_out_row_stride, heads_apart, _ = _qkv_rows(out, "out", shape, dev)
+        if heads_apart != shape[2] and shape[1] > 1 and rows:
             raise ValueError("out's heads must lie one after the other")
+        shape = (rows, paged.desc.heads, paged.channels)
+        d.k_row_stride, d.k_head_stride, _ = _qkv_rows(k, "k", shape, dev)
+        d.v_row_stride, d.v_head_stride, _ = _qkv_rows(v, "v", shape, dev)
         d.rows = rows
-        d.d_q, d.q_row_stride, d.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
-        d.d_k, d.k_row_stride, d.k_head_stride = k.data_ptr(), k.stride(0), k.stride(1)
-        d.d_v, d.v_row_stride, d.v_head_stride = v.data_ptr(), v.stride(0), v.stride(1)
-        d.d_q_out, d.q_out_row_stride = out.data_ptr(), out.stride(0)
-        d.d_slots, d.d_positions = slots.data_ptr(), _ptr(positions)
-        norms = [None if t is None else t.data_ptr() + layer * self._layer_bytes for t in self._norms]
-        d.d_q_norm, d.d_k_norm = norms
+        d.d_q, d.d_k, d.d_v, d.d_q_out = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
+        d.d_slots = slots.data_ptr()
+        q_norm, k_norm = self._norms
+        d.d_q_norm = None if q_norm is None else q_norm + layer * self._layer_bytes
+        d.d_k_norm = None if k_norm is None else k_norm + layer * self._layer_bytes
         st = _queue(dev, stream, lambda s: _lib_qkv(paged.ref, layer, self._ref, s), q, k, v, slots, positions, out,
                     *(paged.pools if stream is not None else ()), own=self._own)
         _check(st, "kvc_paged_qkv")
@@ -897,9 +900,11 @@ class DraftVerifier:
         self.workspace = self._own[1]
 
     def _rows_of(self, t, name, rows):
-        if t.dtype != torch.float32 or t.device != self.device or t.shape != (rows, self.vocab) or \
-                (self.vocab > 1 and rows and t.stride(1) != 1):
+        s = t.stride()
+        if t.dtype is not torch.float32 or t.shape != (rows, self.vocab) or t.device != self.device or \
+                (s[1] != 1 and self.vocab > 1 and rows):
             raise ValueError(f"{name} must be float32 [{rows}, {self.vocab}] on {self.device}, a row's values contiguous")
+        return s[0]
 
     def __call__(self, target: torch.Tensor, tokens: torch.Tensor, row_starts: torch.Tensor, accept: torch.Tensor,
                  sample: torch.Tensor, parents: torch.Tensor | None = None, draft: torch.Tensor | None = None,
@@ -924,9 +929,15 @@ class DraftVerifier:
         _tensor(sample, "sample", torch.float32, (self.batch,), dev)
         if parents is not None:
             _tensor(parents, "parents", torch.int32, (rows,), dev)
-        self._rows_of(target, "target", rows)
+            d.d_parents = parents.data_ptr()
+        else:
+            d.d_parents = None
+        d.target_row_stride = self._rows_of(target, "target", rows)
         if draft is not None:
-            self._rows_of(draft, "draft", rows)
+            d.draft_row_stride = self._rows_of(draft, "draft", rows)
+            d.d_draft = draft.data_ptr()
+        else:
+            d.d_draft = None
         if kept is None or kept_lens is None or out_tokens is None:
             with torch.cuda.stream(stream):
                 make = lambda n, t: torch.empty(n, dtype=torch.int32, device=dev) if t is None else t
@@ -935,9 +946,7 @@ class DraftVerifier:
         _tensor(kept_lens, "kept_lens", torch.int32, (self.batch,), dev)
         _tensor(out_tokens, "out_tokens", torch.int32, (rows,), dev)
         d.rows = rows
-        d.d_row_starts, d.d_tokens, d.d_parents = row_starts.data_ptr(), tokens.data_ptr(), _ptr(parents)
-        d.d_target, d.target_row_stride = target.data_ptr(), target.stride(0)
-        d.d_draft, d.draft_row_stride = _ptr(draft), 0 if draft is None else draft.stride(0)
+        d.d_row_starts, d.d_tokens, d.d_target = row_starts.data_ptr(), tokens.data_ptr(), target.data_ptr()
         d.d_accept, d.d_sample = accept.data_ptr(), sample.data_ptr()
         d.d_kept, d.d_kept_lens, d.d_out_tokens = kept.data_ptr(), kept_lens.data_ptr(), out_tokens.data_ptr()
         ws = self.workspace
