@@ -128,22 +128,16 @@ hipError_t launch_compact(const CompactArgs& a, hipStream_t s);
 constexpr int kMaxShared = 1024;        // requests of a fork or release
 
 // Head of the workspace of forks and releases (zero before the first); behind
-// it (at 256) a fork's entries, then a bit a page, zero between releases.
+// it the places that workgroups count in, 256 bytes apart, 0 between calls,
+// and a bit a page, zero between releases.
+constexpr int kArrivals = 16, kArrivalStride = 64;
+constexpr uint64_t kSharedBits = 256 + 4 * kArrivals * kArrivalStride;
 struct SharedControl {
     uint32_t magic;
     uint32_t flags;                     // of the last call
-    uint32_t pending;                   // of a release under way, 0 between
-    int32_t entries;                    // of a fork
+    uint32_t pending;                   // of a call under way, 0 between
+    uint32_t arrived;                   // places whose workgroups are all done, 0 between
 };
-struct ForkEntry {
-    int32_t parent, child;
-    int32_t whole, rest;                // the parent's full pages; tokens of its last one
-    int32_t page;                       // the page that these are copied to; -1: none
-    int32_t from;                       // ... and from
-};
-constexpr uint64_t kSharedEntries = 256;
-constexpr uint64_t kSharedBits = kSharedEntries + sizeof(ForkEntry) * kMaxShared;
-static_assert(kSharedBits == 256 + 24 * 1024, "KVC_SHARED_PAGES_WORKSPACE_BYTES");
 struct SharedArgs {
     PagesOf g;
     int32_t* table;
@@ -159,7 +153,7 @@ struct SharedArgs {
     const int32_t* children;            // ... or the requests released
     const int32_t* context;             // forks; null: none has any
     SharedControl* ctl;
-    ForkEntry* entries;
+    uint32_t* arrivals;
     uint32_t* bits;
 };
 hipError_t launch_fork(const SharedArgs& a, hipStream_t s);

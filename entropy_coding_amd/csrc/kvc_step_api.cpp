@@ -95,7 +95,7 @@ kvc::SharedArgs shared_args(const kvc_paged_kv* g, int32_t kv_dtype, int64_t cha
     a.children = nullptr;
     a.context = nullptr;
     a.ctl = static_cast<kvc::SharedControl*>(d_workspace);
-    a.entries = reinterpret_cast<kvc::ForkEntry*>(ws + kvc::kSharedEntries);
+    a.arrivals = reinterpret_cast<uint32_t*>(ws + 256);
     a.bits = reinterpret_cast<uint32_t*>(ws + kvc::kSharedBits);
     return a;
 }

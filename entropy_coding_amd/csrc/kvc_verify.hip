@@ -31,22 +31,22 @@ __device__ Units units_of(float y) {
 // What is no number between 0 and 1 counts as the nearer of them, NaN as 0.
 __device__ float clean(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }
 
-// What is left of a probability p after `rejected` siblings drawn with
-// probability q were rejected: each rejection takes q off and the next
-// sibling meets the rest scaled to a sum of 1.
-__device__ float left_of(float p, float q, const float* scales, int rejected) {
-    float y = p;
+// What is left of probabilities after `rejected` siblings drawn with
+// probabilities q were rejected: each rejection takes q off, and the next
+// sibling meets the rest scaled to a sum of 1 (scales[k], k > 0).
+template <int N>
+__device__ void reject(float (&y)[N], const float (&q)[N], const float* scales, int rejected) {
     for (int k = 0; k < rejected; ++k) {
-        if (k) y *= scales[k];
-        y = fmaxf(y - q, 0.0f);
+        const float s = k ? scales[k] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = fmaxf(y[i] * s - q[i], 0.0f);
     }
-    return y;
 }
 
 typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));     // (a row may begin at any value)
 
 // Four values of a row from `at` on, 0 behind its end.
-__device__ void load4(const float* row, uint32_t at, uint32_t vocab, float (&x)[4]) {
+__device__ void load4(const float* row, uint32_t at, uint32_t vocab, float* x) {
     if (at + 4 <= vocab) {
         const float4u y = *reinterpret_cast<const float4u*>(row + at);
 #pragma unroll
@@ -158,8 +158,10 @@ __device__ void walk(const VerifyArgs& a, const Tree& t, Walk& w, bool writes, S
             if (a.draft) {
                 float y = p;
                 if (rejected) {
-                    const float s = scale(current, rejected);
-                    y = left_of(p, q, w.scales, rejected) * s;
+                    const float s = scale(current, rejected), one[1] = {q};
+                    float rest[1] = {p};
+                    reject(rest, one, w.scales, rejected);
+                    y = rest[0] * s;
                 }
                 ok = u * double(q) < double(y);
             } else {
@@ -231,16 +233,15 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyArgs a) {
         const float* const draft = a.draft + (t.start + current) * a.draft_row;
         Units sum{0, 0};
         for (uint32_t at = 4 * tid; at < a.vocab; at += 4 * kAtOnce * kWalkThreads) {
-            float x[kAtOnce][4], y[kAtOnce][4];
+            float x[4 * kAtOnce], q[4 * kAtOnce];
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
-                load4(target, at + 4 * kWalkThreads * k, a.vocab, x[k]);
-                load4(draft, at + 4 * kWalkThreads * k, a.vocab, y[k]);
+                load4(target, at + 4 * kWalkThreads * k, a.vocab, x + 4 * k);
+                load4(draft, at + 4 * kWalkThreads * k, a.vocab, q + 4 * k);
             }
+            reject(x, q, w.scales, rejected);
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum.add(units_of(left_of(x[k][e], y[k][e], w.scales, rejected)));
+            for (int i = 0; i < 4 * kAtOnce; ++i) sum.add(units_of(x[i]));
         }
         const uint64_t z = block_sum<kWalkThreads>(sum, of_wave);
         const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
@@ -267,6 +268,7 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyArgs a) {
 constexpr int kDrawThreads = 256;
 constexpr int kDrawWaves = kDrawThreads / 64;
 constexpr int kGroups = kVerifyChunk / (4 * kDrawThreads);
+constexpr int kValues = 4 * kGroups;            // of a chunk in a thread
 constexpr int kMostChunks = 64;                 // of a workgroup
 
 // What is left of the values of a chunk that a thread has, and their units
@@ -284,34 +286,27 @@ template <bool IN_ORDER>
 __device__ uint32_t place_of(uint32_t tid, int g) { return IN_ORDER ? 4 * (kGroups * tid + g) : 4 * (kDrawThreads * g + tid); }
 
 template <bool IN_ORDER>
-__device__ void chunk_of(const VerifyArgs& a, const Draw& d, uint32_t chunk, float (&x)[kGroups][4], float (&left)[kGroups][4]) {
+__device__ void chunk_of(const VerifyArgs& a, const Draw& d, uint32_t chunk, float (&x)[kValues], float (&left)[kValues]) {
     const uint32_t base = chunk * kVerifyChunk, tid = threadIdx.x;
     const float* const target = a.target + d.stop * a.target_row;
+    const bool both = a.draft && d.rejected > 0;
+    float q[kValues];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) load4(target, base + place_of<IN_ORDER>(tid, g), a.vocab, x[g]);
-    if (a.draft && d.rejected > 0) {
+    for (int g = 0; g < kGroups; ++g) load4(target, base + place_of<IN_ORDER>(tid, g), a.vocab, x + 4 * g);
+    if (both) {
         const float* const draft = a.draft + d.stop * a.draft_row;
-        float q[kGroups][4];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) load4(draft, base + place_of<IN_ORDER>(tid, g), a.vocab, q[g]);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) left[g][e] = left_of(x[g][e], q[g][e], d.scales, d.rejected);
-        return;
+        for (int g = 0; g < kGroups; ++g) load4(draft, base + place_of<IN_ORDER>(tid, g), a.vocab, q + 4 * g);
     }
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) left[g][e] = x[g][e];
+    for (int i = 0; i < kValues; ++i) left[i] = x[i];
+    if (both) reject(left, q, d.scales, d.rejected);
     if (a.draft) return;
     for (int k = 0; k < d.rejected; ++k) {      // tokens that are out
         const uint32_t at = static_cast<uint32_t>(d.rejects[k]) - base;
         if (at >= uint32_t(kVerifyChunk)) continue;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) left[g][e] = at == place_of<IN_ORDER>(tid, g) + e ? 0.0f : left[g][e];
+        for (int i = 0; i < kValues; ++i) left[i] = at == place_of<IN_ORDER>(tid, i / 4) + i % 4 ? 0.0f : left[i];
     }
 }
 
@@ -360,22 +355,22 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
             if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
             return;
         }
-        d = Draw{s.stop, s.rejected, a.scales + s.start, nullptr};
+        for (int k = tid; k < s.rejected; k += kDrawThreads) w.scales[k] = a.scales[s.start + k];
+        __syncthreads();
+        d = Draw{s.stop, s.rejected, w.scales, nullptr};
         last = s.last;
     }
-    float x[kGroups][4], left[kGroups][4];
+    float x[kValues], left[kValues];
     const uint32_t first_chunk = part * per;
     const uint32_t count = first_chunk + per <= a.chunks ? per : a.chunks - first_chunk;
     for (uint32_t c = 0; c < count; ++c) {
         chunk_of<false>(a, d, first_chunk + c, x, left);
         Units before{0, 0}, after{0, 0};
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                before.add(units_of(x[g][e]));
-                after.add(units_of(left[g][e]));
-            }
+        for (int i = 0; i < kValues; ++i) {
+            before.add(units_of(x[i]));
+            after.add(units_of(left[i]));
+        }
         // (a wave's 1024 values pass no 32 bits: see block_sum)
         const uint64_t sum[2] = {Units{scan(after.high), scan(after.low)}.all(), Units{scan(before.high), scan(before.low)}.all()};
         if (lane == 63) {
@@ -456,12 +451,10 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
     chunk_of<true>(a, d, there, x, left);
     Units here{0, 0};
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (which) left[g][e] = x[g][e];
-            here.add(units_of(left[g][e]));
-        }
+    for (int i = 0; i < kValues; ++i) {
+        if (which) left[i] = x[i];
+        here.add(units_of(left[i]));
+    }
     uint64_t sum = Units{scan(here.high), scan(here.low)}.all();
     if (lane == 63) of_value[wave] = sum;
     __syncthreads();
@@ -472,11 +465,11 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
     if (sum <= point && point < sum + here.all()) {
         int at = 0;
 #pragma unroll
-        for (int i = 0; i < 4 * kGroups - 1; ++i) {
-            sum += units_of(left[i / 4][i % 4]).all();
+        for (int i = 0; i < kValues - 1; ++i) {
+            sum += units_of(left[i]).all();
             if (sum <= point) at = i + 1;
         }
-        a.out_tokens[last] = static_cast<int32_t>(there * kVerifyChunk + 4 * kGroups * tid + at);
+        a.out_tokens[last] = static_cast<int32_t>(there * kVerifyChunk + kValues * tid + at);
         a.words[2 * b + 1] = 0u;
     }
     if (WALKS) write_walk<kDrawThreads>(a, t, w, b);
