@@ -59,9 +59,29 @@ struct Pieces {
     }
 };
 
-// One row's heads (queries, then keys, then values), as many at a time as a
-// wave has groups of lanes.
-template <int D, bool FP8, bool NEIGHBOURS>
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <class T>
+using Global = __attribute__((address_space(1))) T;     // (a pool's pointer, read from memory, says nothing of it)
+
+enum : uint32_t { kQuery, kKey, kValue };
+
+// Two float32 values as e4m3 of x / scale, the scale given as its reciprocal
+// in float64: the product rounded to float32 is the quotient of a bf16 value
+// to the last bit (such a quotient lies further from the middle of two float32
+// values, 2^-49 of itself, than the product is off), and takes a third of the
+// instructions of a division.
+__device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
+    const float x = static_cast<float>(double(lo) * per_scale), y = static_cast<float>(double(hi) * per_scale);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(clamp448(x), clamp448(y), 0, false)) & 0xFFFFu;
+}
+
+// A row's heads (queries, then keys, then values), as many at a time as a wave
+// has groups of lanes; UNIFORM: all of a step's heads are of one kind.  The
+// next step's values are asked for before this one's are looked at, a row's
+// first ones before its position.  An angle's sine and cosine are formed once
+// a row, one in a lane, and handed round through LDS.
+template <int D, bool FP8, bool NEIGHBOURS, bool UNIFORM>
 __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
     constexpr int kUnits = D / 16;              // lanes that a head needs
     constexpr int kGroup = kUnits == 12 ? 16 : kUnits;
@@ -75,9 +95,38 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
     const uint32_t all = a.q_heads + 2 * a.heads, steps = (all + kHeads - 1) / kHeads;
     const uint32_t per = (steps + a.parts - 1) / a.parts;
     const int64_t items = a.rows * a.parts;
+
+    struct Step {
+        uint32_t kind, head;
+        bool real;
+    };
+    const auto step_of = [&](uint32_t step) {
+        const uint32_t begin = step * kHeads;
+        Step r;
+        const uint32_t index = UNIFORM ? begin : begin + group;
+        r.kind = index < a.q_heads ? kQuery : index < a.q_heads + a.heads ? kKey : kValue;
+        r.head = index - (r.kind == kQuery ? 0 : r.kind == kKey ? a.q_heads : a.q_heads + a.heads) + (UNIFORM ? group : 0);
+        r.real = here && (UNIFORM || index < all);
+        return r;
+    };
+    const auto fetch = [&](int64_t row, uint32_t step) {
+        const Step t = step_of(step);
+        const HeadRows from = t.kind == kQuery ? a.q : t.kind == kKey ? a.k : a.v;
+        Pieces in{};
+        if (t.real) {
+            const uint16_t* const x = from.at + row * from.row + int64_t(t.head) * from.head;
+            in.raw[0] = *reinterpret_cast<const uint4*>(x + first);
+            in.raw[1] = *reinterpret_cast<const uint4*>(x + second);
+        }
+        return in;
+    };
+
     for (int64_t item = int64_t(blockIdx.x) * kQkvWaves + wave; item < items; item += int64_t(gridDim.x) * kQkvWaves) {
         const int64_t row = a.parts == 1 ? item : item / a.parts;
         const uint32_t part = static_cast<uint32_t>(item - row * a.parts);
+        const uint32_t begin = part * per, end = begin + per < steps ? begin + per : steps;
+        if (begin >= end) continue;
+        Pieces next = fetch(row, begin);
         const int32_t position = a.positions ? a.positions[row] : 0;
         if (position < 0) continue;
         const int64_t slot = a.slots[row];
@@ -97,41 +146,20 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t at = NEIGHBOURS ? (i < 4 ? 4 * u + i : half / 2 + 4 * u + i - 4) : 8 * u + i;
-                const float2 t = turned ? turns[wave][at] : float2{1.0f, 0.0f};
+                const float2 t = turns[wave][turned ? at : 0];
                 c[i] = t.x;
                 s[i] = t.y;
             }
             __builtin_amdgcn_wave_barrier();
         }
-        const uint32_t end = (part + 1) * per < steps ? (part + 1) * per : steps;
-        for (uint32_t step = part * per; step < end; ++step) {
-            const uint32_t index = step * kHeads + group;
-            const int kind = index < a.q_heads ? 0 : index < a.q_heads + a.heads ? 1 : 2;
-            const uint32_t head = kind == 0 ? index : kind == 1 ? index - a.q_heads : index - a.q_heads - a.heads;
-            const bool real = here && index < all;
-            const HeadRows from = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-            Pieces in{};
-            if (real) {
-                const uint16_t* const x = from.at + row * from.row + int64_t(head) * from.head;
-                in.raw[0] = *reinterpret_cast<const uint4*>(x + first);
-                in.raw[1] = *reinterpret_cast<const uint4*>(x + second);
-            }
+        for (uint32_t step = begin; step < end; ++step) {
+            const Pieces in = next;
+            if (step + 1 < end) next = fetch(row, step + 1);
+            const Step t = step_of(step);
             float x[2][8];
             in.unpack(x);
-            const void* const norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+            const void* const norm = t.kind == kQuery ? a.q_norm : t.kind == kKey ? a.k_norm : nullptr;
             if (norm) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sum = fmaf(x[i / 8][i % 8], x[i / 8][i % 8], sum);
-                sum = group_sum<kGroup>(sum);
-                float r = __builtin_amdgcn_rsqf(fmaf(sum, 1.0f / D, a.eps));
-                if (__any(sum > 3.0e38f)) {     // squares beyond float32
-                    double wide = 0.0;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) wide = fma(double(x[i / 8][i % 8]), double(x[i / 8][i % 8]), wide);
-                    wide = group_sum<kGroup>(wide);
-                    if (sum > 3.0e38f) r = static_cast<float>(1.0 / sqrt(wide / D + double(a.eps)));
-                }
                 float w[2][8];
                 if (a.norm_f32) {
 #pragma unroll
@@ -152,63 +180,90 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
                     }
                     y.unpack(w);
                 }
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum = fmaf(x[i / 8][i % 8], x[i / 8][i % 8], sum);
+                sum = group_sum<kGroup>(sum);
+                float r = __builtin_amdgcn_rsqf(fmaf(sum, 1.0f / D, a.eps));
+                if (__any(sum > 3.0e38f)) {     // squares beyond float32
+                    double wide = 0.0;
+#pragma nounroll
+                    for (int i = 0; i < 8; ++i) {
+                        float y[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k == i) {
+                                y[0] = x[0][k];
+                                y[1] = x[1][k];
+                            }
+                        wide = fma(double(y[1]), double(y[1]), fma(double(y[0]), double(y[0]), wide));
+                    }
+                    wide = group_sum<kGroup>(wide);
+                    if (sum > 3.0e38f) r = static_cast<float>(1.0 / sqrt(wide / D + double(a.eps)));
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i / 8][i % 8] = x[i / 8][i % 8] * r * w[i / 8][i % 8];
             }
-            if (turned && kind != 2) {
+            if (turned && t.kind != kValue) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float& left = NEIGHBOURS ? x[i / 4][2 * (i % 4)] : x[0][i];
                     float& right = NEIGHBOURS ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
-                    const float l = fmaf(left, c[i], -(right * s[i])), t = fmaf(left, s[i], right * c[i]);
+                    const float l = fmaf(left, c[i], -(right * s[i])), y = fmaf(left, s[i], right * c[i]);
                     left = l;
-                    right = t;
+                    right = y;
                 }
             }
-            if (!real) continue;
-            if (kind != 0 && (slot < 0 || slot >= a.n_slots)) continue;
-            uint8_t* to = reinterpret_cast<uint8_t*>(a.out + row * a.out_row + int64_t(head) * D);
-            if (kind != 0)
-                to = static_cast<uint8_t*>(a.pools[kind - 1]) + (slot * a.heads + head) * int64_t(D) * (FP8 ? 1 : 2);
-            if (FP8 && kind != 0) {
-                const float scale = kind == 1 ? a.k_scale : a.v_scale;
+            if (!t.real) continue;
+            if (t.kind != kQuery && (slot < 0 || slot >= a.n_slots)) continue;
+            Global<uint8_t>* to;
+            if (t.kind == kQuery)
+                to = (Global<uint8_t>*)(a.out + row * a.out_row + int64_t(t.head) * D);
+            else
+                to = (Global<uint8_t>*)(a.pools[t.kind - kKey]) + (slot * a.heads + t.head) * int64_t(D) * (FP8 ? 1 : 2);
+            if (FP8 && t.kind != kQuery) {
+                const double per_scale = t.kind == kKey ? a.per_k_scale : a.per_v_scale;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    uint32_t w[2];
+                    u32x2 y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        w[i] = round_two(x[p][4 * i], x[p][4 * i + 1], scale) |
-                               (round_two(x[p][4 * i + 2], x[p][4 * i + 3], scale) << 16);
-                    *reinterpret_cast<uint2*>(to + (p ? second : first)) = uint2{w[0], w[1]};
+                        y[i] = round_scaled(x[p][4 * i], x[p][4 * i + 1], per_scale) |
+                               (round_scaled(x[p][4 * i + 2], x[p][4 * i + 3], per_scale) << 16);
+                    *(Global<u32x2>*)(to + (p ? second : first)) = y;
                 }
             } else {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    uint4 y = in.raw[p];
-                    if (kind != 2)
-                        y = uint4{two_bf16(x[p][0], x[p][1]), two_bf16(x[p][2], x[p][3]),
+                    u32x4 y = {in.raw[p].x, in.raw[p].y, in.raw[p].z, in.raw[p].w};     // (values keep every bit)
+                    if (t.kind != kValue)
+                        y = u32x4{two_bf16(x[p][0], x[p][1]), two_bf16(x[p][2], x[p][3]),
                                   two_bf16(x[p][4], x[p][5]), two_bf16(x[p][6], x[p][7])};
-                    *reinterpret_cast<uint4*>(to + 2 * (p ? second : first)) = y;
+                    *(Global<u32x4>*)(to + 2 * (p ? second : first)) = y;
                 }
             }
         }
     }
 }
 
-template <int D>
-hipError_t launch(const QkvArgs& args, bool fp8, bool neighbours, hipStream_t s) {
+template <int D, bool FP8, bool NEIGHBOURS>
+hipError_t launch(const QkvArgs& args, hipStream_t s) {
     QkvArgs a = args;
     constexpr int kHeads = 64 / (D == 192 ? 16 : D / 16);
     const int64_t steps = (int64_t(a.q_heads) + 2 * int64_t(a.heads) + kHeads - 1) / kHeads;
-    a.parts = a.rows * steps <= 4096 ? static_cast<uint32_t>(steps) : 1;
+    a.parts = a.rows * steps <= 4096 ? static_cast<uint32_t>(steps) : steps > 2 ? 2 : 1;
     int64_t blocks = (a.rows * a.parts + kQkvWaves - 1) / kQkvWaves;
     if (blocks > 1 << 16) blocks = 1 << 16;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(64 * kQkvWaves);
-    if (fp8 && neighbours) k_qkv<D, true, true><<<grid, block, 0, s>>>(a);
-    else if (fp8) k_qkv<D, true, false><<<grid, block, 0, s>>>(a);
-    else if (neighbours) k_qkv<D, false, true><<<grid, block, 0, s>>>(a);
-    else k_qkv<D, false, false><<<grid, block, 0, s>>>(a);
+    if (a.q_heads % kHeads == 0 && a.heads % kHeads == 0) k_qkv<D, FP8, NEIGHBOURS, true><<<grid, block, 0, s>>>(a);
+    else k_qkv<D, FP8, NEIGHBOURS, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch(const QkvArgs& a, bool fp8, bool neighbours, hipStream_t s) {
+    if (fp8) return neighbours ? launch<D, true, true>(a, s) : launch<D, true, false>(a, s);
+    return neighbours ? launch<D, false, true>(a, s) : launch<D, false, false>(a, s);
 }
 
 }  // namespace

@@ -29,7 +29,8 @@ struct QkvArgs {
     uint32_t q_heads, heads, rotary;
     uint32_t norm_f32;                  // the norms' weights are float32 (bf16 otherwise)
     uint32_t parts;                     // that a row's heads are split into (the launch sets it)
-    float eps, k_scale, v_scale;
+    float eps;
+    double per_k_scale, per_v_scale;    // 1 / scale
 };
 hipError_t launch_qkv(const QkvArgs& args, int64_t channels, bool fp8, bool neighbours, hipStream_t s);
 

@@ -148,8 +148,8 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
     a.norm_f32 = p->norm_dtype == KVC_F32;
     a.parts = 1;
     a.eps = p->eps;
-    a.k_scale = p->k_scale;
-    a.v_scale = p->v_scale;
+    a.per_k_scale = 1.0 / double(p->k_scale);
+    a.per_v_scale = 1.0 / double(p->v_scale);
     return kvc::launch_qkv(a, p->channels, p->kv_dtype == KVC_E4M3, p->neighbours != 0,
                            static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
 }
