@@ -40,10 +40,10 @@ __device__ T group_sum(T x) {
     return x;
 }
 
-// Sixteen channels of a head in a lane: two pieces of eight.  Among the first
-// `rotary` channels the second piece lies half of them behind the first, so
-// that a lane has both values of every pair, whether pairs are such halves or
-// neighbours; behind them the pieces follow each other.
+// Sixteen channels of a head in a lane: two pieces of eight, so that a lane
+// has both values of every pair.  Where a channel's other one lies half of the
+// `rotary` channels behind it, so does the second piece behind the first; else
+// the pieces follow each other.
 struct Pieces {
     uint4 raw[2];
     __device__ void unpack(float (&x)[2][8]) const {
@@ -82,7 +82,7 @@ __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
 // first ones before its position.  An angle's sine and cosine are formed once
 // a row, one in a lane, and handed round through LDS.
 template <int D, bool FP8, bool NEIGHBOURS, bool UNIFORM>
-__global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
+__global__ __launch_bounds__(64 * kQkvWaves, 4) void k_qkv(QkvArgs a) {
     constexpr int kUnits = D / 16;              // lanes that a head needs
     constexpr int kGroup = kUnits == 12 ? 16 : kUnits;
     constexpr int kHeads = 64 / kGroup;
@@ -91,7 +91,8 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
     const uint32_t u = lane % kGroup, group = lane / kGroup;
     const uint32_t half = a.rotary / 2, rotated = a.rotary / 16;
     const bool here = u < kUnits, turned = u < rotated;
-    const uint32_t first = turned ? 8 * u : 16 * u, second = turned ? half + 8 * u : 16 * u + 8;
+    const bool apart = turned && !NEIGHBOURS;
+    const uint32_t first = apart ? 8 * u : 16 * u, second = apart ? half + 8 * u : 16 * u + 8;
     const uint32_t all = a.q_heads + 2 * a.heads, steps = (all + kHeads - 1) / kHeads;
     const uint32_t per = (steps + a.parts - 1) / a.parts;
     const int64_t items = a.rows * a.parts;
@@ -145,8 +146,7 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t at = NEIGHBOURS ? (i < 4 ? 4 * u + i : half / 2 + 4 * u + i - 4) : 8 * u + i;
-                const float2 t = turns[wave][turned ? at : 0];
+                const float2 t = turns[wave][turned ? 8 * u + i : 0];
                 c[i] = t.x;
                 s[i] = t.y;
             }
@@ -223,14 +223,17 @@ __global__ __launch_bounds__(64 * kQkvWaves) void k_qkv(QkvArgs a) {
                 to = (Global<uint8_t>*)(a.pools[t.kind - kKey]) + (slot * a.heads + t.head) * int64_t(D) * (FP8 ? 1 : 2);
             if (FP8 && t.kind != kQuery) {
                 const double per_scale = t.kind == kKey ? a.per_k_scale : a.per_v_scale;
+                u32x4 y;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    u32x2 y;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        y[i] = round_scaled(x[p][4 * i], x[p][4 * i + 1], per_scale) |
-                               (round_scaled(x[p][4 * i + 2], x[p][4 * i + 3], per_scale) << 16);
-                    *(Global<u32x2>*)(to + (p ? second : first)) = y;
+                for (int i = 0; i < 4; ++i) {
+                    const float* const four = x[i / 2] + 4 * (i % 2);
+                    y[i] = round_scaled(four[0], four[1], per_scale) | (round_scaled(four[2], four[3], per_scale) << 16);
+                }
+                if (apart) {
+                    *(Global<u32x2>*)(to + first) = u32x2{y[0], y[1]};
+                    *(Global<u32x2>*)(to + second) = u32x2{y[2], y[3]};
+                } else {
+                    *(Global<u32x4>*)(to + first) = y;
                 }
             } else {
 #pragma unroll
