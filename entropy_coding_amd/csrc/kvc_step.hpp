@@ -42,36 +42,25 @@ constexpr int kVerifyChunk = 4096;      // values of a distribution that a workg
 
 // Head of the workspace; behind it two words a sequence (what the walk and
 // the draw found wrong), the workgroups of a sequence that are done (0 before
-// the first call and between calls), a VerifyState each and the scales between
-// the rejections at the node where a sequence stops, by row (both where a
-// kernel of its own walks), and the chunks' sums.
+// the first call and between calls) and the chunks' sums.
 struct VerifyControl {
     uint32_t magic;
     uint32_t batch;
-};
-struct VerifyState {                    // where a sequence stops
-    int32_t start, rows;                // rows 0: nothing to draw
-    int32_t stop;                       // row of the node
-    int32_t last;                       // row of the drawn token in out_tokens
-    int32_t rejected;                   // entries of its scales
-    int32_t pad[3];
 };
 struct VerifySums {                     // units of 2^-42
     uint64_t left, whole;               // after the rejections, and before
 };
 struct VerifyLayout {
-    uint64_t words, arrived, states, scales, sums, total;
+    uint64_t words, arrived, sums, total;
     uint32_t chunks;
 };
-inline VerifyLayout verify_layout(int64_t batch, int64_t rows, int64_t vocab) {
+inline VerifyLayout verify_layout(int64_t batch, int64_t vocab) {
     const auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
     VerifyLayout l;
     l.chunks = static_cast<uint32_t>((vocab + kVerifyChunk - 1) / kVerifyChunk);
     l.words = 256;
     l.arrived = l.words + up(8 * uint64_t(batch));
-    l.states = l.arrived + up(4 * uint64_t(batch));
-    l.scales = l.states + up(sizeof(VerifyState) * uint64_t(batch));
-    l.sums = l.scales + up(4 * uint64_t(rows));
+    l.sums = l.arrived + up(4 * uint64_t(batch));
     l.total = l.sums + up(sizeof(VerifySums) * uint64_t(batch) * l.chunks);
     return l;
 }
@@ -92,8 +81,6 @@ struct VerifyArgs {
     VerifyControl* ctl;
     uint32_t* words;
     uint32_t* arrived;
-    VerifyState* states;
-    float* scales;
     VerifySums* sums;
 };
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);

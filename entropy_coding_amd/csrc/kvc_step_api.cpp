@@ -156,7 +156,7 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
 
 int kvc_verify_drafts_sizes(const kvc_drafts* p, uint64_t* h_workspace_bytes) {
     if (!h_workspace_bytes || !verify_sizes_ok(p)) return KVC_ERR_INVALID;
-    *h_workspace_bytes = kvc::verify_layout(p->batch, p->rows, p->vocab).total;
+    *h_workspace_bytes = kvc::verify_layout(p->batch, p->vocab).total;
     return KVC_OK;
 }
 
@@ -172,7 +172,7 @@ int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace
                           static_cast<const void*>(p->d_kept_lens), static_cast<const void*>(p->d_out_tokens)})
         if (!aligned(d, 4)) return KVC_ERR_INVALID;
     if (!stride_ok(p->target_row_stride) || (p->d_draft && !stride_ok(p->draft_row_stride))) return KVC_ERR_INVALID;
-    const kvc::VerifyLayout l = kvc::verify_layout(p->batch, p->rows, p->vocab);
+    const kvc::VerifyLayout l = kvc::verify_layout(p->batch, p->vocab);
     if (workspace_bytes < l.total) return KVC_ERR_CAPACITY;
     char* const ws = static_cast<char*>(d_workspace);
     kvc::VerifyArgs a;
@@ -194,9 +194,7 @@ int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace
     a.out_tokens = p->d_out_tokens;
     a.ctl = static_cast<kvc::VerifyControl*>(d_workspace);
     a.words = reinterpret_cast<uint32_t*>(ws + l.words);
-    a.states = reinterpret_cast<kvc::VerifyState*>(ws + l.states);
     a.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
-    a.scales = reinterpret_cast<float*>(ws + l.scales);
     a.sums = reinterpret_cast<kvc::VerifySums*>(ws + l.sums);
     return kvc::launch_verify(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
 }

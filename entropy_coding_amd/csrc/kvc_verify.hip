@@ -215,98 +215,42 @@ __device__ void write_walk(const VerifyArgs& a, const Tree& t, const Walk& w, in
     }
 }
 
-constexpr int kWalkThreads = 1024;
-
-// The walk of trees whose nodes were drawn from the draft's probabilities, a
-// workgroup a sequence: before a sibling of a rejected node is tested, all of
-// it sums what the rejections left over the vocabulary.  Bound by the trips to
-// memory of each such sum: a thread has eight loads under way.
-__global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyArgs a) {
-    constexpr int kAtOnce = 4;
-    __shared__ Walk w;
-    __shared__ uint64_t of_wave[kWalkThreads / 64];
-    const int64_t b = blockIdx.x;
-    const int tid = threadIdx.x;
-    const Tree t = tree_of(a, b);
-    const auto scale = [&](int current, int rejected) {
-        const float* const target = a.target + (t.start + current) * a.target_row;
-        const float* const draft = a.draft + (t.start + current) * a.draft_row;
-        Units sum{0, 0};
-        for (uint32_t at = 4 * tid; at < a.vocab; at += 4 * kAtOnce * kWalkThreads) {
-            float x[4 * kAtOnce], q[4 * kAtOnce];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                load4(target, at + 4 * kWalkThreads * k, a.vocab, x + 4 * k);
-                load4(draft, at + 4 * kWalkThreads * k, a.vocab, q + 4 * k);
-            }
-            reject(x, q, w.scales, rejected);
-#pragma unroll
-            for (int i = 0; i < 4 * kAtOnce; ++i) sum.add(units_of(x[i]));
-        }
-        const uint64_t z = block_sum<kWalkThreads>(sum, of_wave);
-        const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
-        if (tid == 0) w.scales[rejected] = s;
-        __syncthreads();
-        return s;
-    };
-    if (t.n) walk(a, t, w, tid == 0, scale, [] { __syncthreads(); });
-    __syncthreads();
-    write_walk<kWalkThreads>(a, t, w, b);
-    if (tid == 0) {
-        VerifyState s{0, 0, 0, 0, 0, {0, 0, 0}};
-        if (t.n)
-            s = VerifyState{static_cast<int32_t>(t.start), t.n, static_cast<int32_t>(t.start) + w.current,
-                            static_cast<int32_t>(t.start) + w.kept - 1, w.rejected, {0, 0, 0}};
-        a.states[b] = s;
-    }
-    if (t.n)
-        for (int k = tid; k < w.rejected; k += kWalkThreads) a.scales[t.start + k] = k ? w.scales[k] : 0.0f;
-}
-
 // ---- the draw
 
-constexpr int kDrawThreads = 256;
-constexpr int kDrawWaves = kDrawThreads / 64;
-constexpr int kGroups = kVerifyChunk / (4 * kDrawThreads);
-constexpr int kValues = 4 * kGroups;            // of a chunk in a thread
 constexpr int kMostChunks = 64;                 // of a workgroup
 
-// What is left of the values of a chunk that a thread has, and their units
-// before and after the rejections.
+// The distribution that a sequence draws from.
 struct Draw {
     int64_t stop;                               // row of the node
-    int rejected;
+    int rejected;                               // entries of its list
     const float* scales;
     const int32_t* rejects;
 };
-// The value of a chunk that a thread has as the e-th of its g-th four: fours
-// dealt to the threads in turn (for sums), or all of a thread's one after the
-// other (IN_ORDER).
-template <bool IN_ORDER>
-__device__ uint32_t place_of(uint32_t tid, int g) { return IN_ORDER ? 4 * (kGroups * tid + g) : 4 * (kDrawThreads * g + tid); }
 
-template <bool IN_ORDER>
-__device__ void chunk_of(const VerifyArgs& a, const Draw& d, uint32_t chunk, float (&x)[kValues], float (&left)[kValues]) {
-    const uint32_t base = chunk * kVerifyChunk, tid = threadIdx.x;
+// N values of a row from `base` on, in fours at place(0), place(1), ..., 0 from
+// `end` on; and what the rejections left of them.
+template <int THREADS, int N, class Place>
+__device__ void values_of(const VerifyArgs& a, const Draw& d, uint32_t base, uint32_t end, Place place, float (&x)[N],
+                          float (&left)[N]) {
     const float* const target = a.target + d.stop * a.target_row;
     const bool both = a.draft && d.rejected > 0;
-    float q[kValues];
+    float q[N];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) load4(target, base + place_of<IN_ORDER>(tid, g), a.vocab, x + 4 * g);
+    for (int g = 0; g < N / 4; ++g) load4(target, base + place(g), end, x + 4 * g);
     if (both) {
         const float* const draft = a.draft + d.stop * a.draft_row;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) load4(draft, base + place_of<IN_ORDER>(tid, g), a.vocab, q + 4 * g);
+        for (int g = 0; g < N / 4; ++g) load4(draft, base + place(g), end, q + 4 * g);
     }
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) left[i] = x[i];
+    for (int i = 0; i < N; ++i) left[i] = x[i];
     if (both) reject(left, q, d.scales, d.rejected);
     if (a.draft) return;
     for (int k = 0; k < d.rejected; ++k) {      // tokens that are out
         const uint32_t at = static_cast<uint32_t>(d.rejects[k]) - base;
-        if (at >= uint32_t(kVerifyChunk)) continue;
+        if (at >= uint32_t(N) * THREADS) continue;
 #pragma unroll
-        for (int i = 0; i < kValues; ++i) left[i] = at == place_of<IN_ORDER>(tid, i / 4) + i % 4 ? 0.0f : left[i];
+        for (int i = 0; i < N; ++i) left[i] = at == place(i / 4) + i % 4 ? 0.0f : left[i];
     }
 }
 
@@ -320,62 +264,77 @@ __device__ uint64_t scan_wide(uint64_t x) {
 
 // Chunks of one sequence's distribution, `per` at a time, are summed by a
 // workgroup; the last workgroup of a sequence to be done draws the token.
-// Chains, and trees without probabilities, are walked by every workgroup for
-// itself (WALKS), by its first wave: a chain of trips to memory as long as a
-// kernel of its own would take, and a launch less.
-template <bool WALKS>
-__global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint32_t parts, uint32_t per) {
+// Every workgroup walks the tree for itself: chains, and trees without
+// probabilities, by its first wave, a chain of trips to memory as long as a
+// kernel of its own would take, and a launch less.  Of trees whose nodes were
+// drawn from the draft's probabilities (DRAWN) what the rejections left is
+// summed over the vocabulary before a sibling of a rejected node is tested, by
+// the whole workgroup; with 1024 threads that is bound by what one CU reads
+// (4.6 us for 32000 tokens).
+template <int THREADS, bool DRAWN>
+__global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts, uint32_t per) {
+    constexpr int kWaves = THREADS / 64, kValues = 16;      // of a thread, asked for together
+    constexpr int kChunksAtOnce = kValues * THREADS / kVerifyChunk;
     __shared__ Walk w;
-    __shared__ uint64_t of_wave[2][kDrawWaves], of_value[kDrawWaves];
-    __shared__ uint64_t of_chunk[2][kMostChunks][kDrawWaves];
+    __shared__ uint64_t of_wave[2][kWaves], of_value[kWaves];
+    __shared__ uint64_t of_chunk[2][kMostChunks][kWaves];
     __shared__ uint32_t place;
     __shared__ uint64_t place_before;
     const uint32_t b = blockIdx.x / parts, part = blockIdx.x - b * parts;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (blockIdx.x == 0 && tid == 0) *a.ctl = VerifyControl{kPagedMagic, static_cast<uint32_t>(a.batch)};
     const float u = a.sample[b];                // (asked for now: a trip less behind the sums)
-    Draw d;
-    Tree t{};
-    int64_t last;                               // of the sequence's new tokens
-    if (WALKS) {
-        t = tree_of(a, b);
-        if (t.n == 0) {
-            if (part == 0) write_walk<kDrawThreads>(a, t, w, b);
-            if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
-            return;
-        }
-        if (wave == 0)
-            walk(a, t, w, tid == 0, [](int, int) { return 0.0f; }, [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); });
-        __syncthreads();
-        d = Draw{t.start + w.current, a.draft ? w.rejected : w.listed, w.scales, w.rejects};
-        last = t.start + w.kept - 1;
-    } else {
-        const VerifyState s = a.states[b];
-        if (s.rows == 0) {
-            if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
-            return;
-        }
-        for (int k = tid; k < s.rejected; k += kDrawThreads) w.scales[k] = a.scales[s.start + k];
-        __syncthreads();
-        d = Draw{s.stop, s.rejected, w.scales, nullptr};
-        last = s.last;
+    const Tree t = tree_of(a, b);
+    if (t.n == 0) {
+        if (part == 0) write_walk<THREADS>(a, t, w, b);
+        if (part == 0 && tid == 0) a.words[2 * b + 1] = 0u;
+        return;
     }
-    float x[kValues], left[kValues];
+    const auto in_turn = [&](int g) { return 4 * (THREADS * g + tid); };
+    if (DRAWN) {
+        const auto scale = [&](int current, int rejected) {
+            const Draw here{t.start + current, rejected, w.scales, nullptr};
+            Units sum{0, 0};
+            for (uint32_t base = 0; base < a.vocab; base += kValues * THREADS) {
+                float x[kValues], left[kValues];
+                values_of<THREADS>(a, here, base, a.vocab, in_turn, x, left);
+#pragma unroll
+                for (int i = 0; i < kValues; ++i) sum.add(units_of(left[i]));
+            }
+            const uint64_t z = block_sum<THREADS>(sum, of_wave[0]);
+            const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
+            if (tid == 0) w.scales[rejected] = s;
+            __syncthreads();
+            return s;
+        };
+        walk(a, t, w, tid == 0, scale, [] { __syncthreads(); });
+    } else if (wave == 0) {
+        walk(a, t, w, tid == 0, [](int, int) { return 0.0f; }, [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); });
+    }
+    __syncthreads();
+    const Draw d{t.start + w.current, a.draft ? w.rejected : w.listed, w.scales, w.rejects};
+    const int64_t last = t.start + w.kept - 1;  // of the sequence's new tokens
     const uint32_t first_chunk = part * per;
     const uint32_t count = first_chunk + per <= a.chunks ? per : a.chunks - first_chunk;
-    for (uint32_t c = 0; c < count; ++c) {
-        chunk_of<false>(a, d, first_chunk + c, x, left);
-        Units before{0, 0}, after{0, 0};
+    const uint32_t here = (first_chunk + count) * kVerifyChunk, end = here < a.vocab ? here : a.vocab;
+    for (uint32_t c = 0; c < count; c += kChunksAtOnce) {
+        float x[kValues], left[kValues];
+        values_of<THREADS>(a, d, (first_chunk + c) * kVerifyChunk, end, in_turn, x, left);
 #pragma unroll
-        for (int i = 0; i < kValues; ++i) {
-            before.add(units_of(x[i]));
-            after.add(units_of(left[i]));
-        }
-        // (a wave's 1024 values pass no 32 bits: see block_sum)
-        const uint64_t sum[2] = {Units{scan(after.high), scan(after.low)}.all(), Units{scan(before.high), scan(before.low)}.all()};
-        if (lane == 63) {
-            of_chunk[0][c][wave] = sum[0];
-            of_chunk[1][c][wave] = sum[1];
+        for (int k = 0; k < kChunksAtOnce; ++k) {
+            constexpr int kOfChunk = kValues / kChunksAtOnce;
+            Units before{0, 0}, after{0, 0};
+#pragma unroll
+            for (int i = k * kOfChunk; i < (k + 1) * kOfChunk; ++i) {
+                before.add(units_of(x[i]));
+                after.add(units_of(left[i]));
+            }
+            // (a wave's 1024 values pass no 32 bits: see block_sum)
+            const uint64_t sum[2] = {Units{scan(after.high), scan(after.low)}.all(), Units{scan(before.high), scan(before.low)}.all()};
+            if (lane == 63 && c + k < count) {
+                of_chunk[0][c + k][wave] = sum[0];
+                of_chunk[1][c + k][wave] = sum[1];
+            }
         }
     }
     __syncthreads();
@@ -385,7 +344,7 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < kDrawWaves; ++k) mine[i] += of_chunk[i][tid][k];
+            for (int k = 0; k < kWaves; ++k) mine[i] += of_chunk[i][tid][k];
     }
     if (parts > 1) {
         // The sums first, as exchanges: what they return says that they are done where all dies see them, with no
@@ -423,7 +382,7 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
     for (int i = 0; i < 2; ++i) {
         total[i] = 0;
 #pragma unroll
-        for (int k = 0; k < kDrawWaves; ++k) {
+        for (int k = 0; k < kWaves; ++k) {
             if (k == int(wave)) upto[i] += total[i];
             total[i] += of_wave[i][k];
         }
@@ -435,64 +394,66 @@ __global__ __launch_bounds__(kDrawThreads) void k_verify_draw(VerifyArgs a, uint
             a.out_tokens[last] = -1;
             a.words[2 * b + 1] = kPagedInvalid;
         }
-        if (WALKS) write_walk<kDrawThreads>(a, t, w, b);
+        write_walk<THREADS>(a, t, w, b);
         return;
     }
     uint64_t point = u > 0.0f ? static_cast<uint64_t>(fmin(double(u), 1.0) * static_cast<double>(all)) : 0;
     if (point >= all) point = all - 1;
-    const uint64_t end = which ? upto[1] : upto[0], first = end - (which ? mine[1] : mine[0]);
-    if (first <= point && point < end) {
+    const uint64_t past = which ? upto[1] : upto[0], first = past - (which ? mine[1] : mine[0]);
+    if (first <= point && point < past) {
         place = tid;
         place_before = first;
     }
     __syncthreads();
-    // ... and there the value
-    const uint32_t there = place;
-    chunk_of<true>(a, d, there, x, left);
-    Units here{0, 0};
+    // ... and there the value, a thread's values one after the other
+    constexpr int kOwn = kVerifyChunk / THREADS;
+    const uint32_t base = place * kVerifyChunk;
+    float x[kOwn], left[kOwn];
+    values_of<THREADS>(a, d, base, a.vocab, [&](int g) { return kOwn * tid + 4 * g; }, x, left);
+    Units own{0, 0};
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) {
+    for (int i = 0; i < kOwn; ++i) {
         if (which) left[i] = x[i];
-        here.add(units_of(left[i]));
+        own.add(units_of(left[i]));
     }
-    uint64_t sum = Units{scan(here.high), scan(here.low)}.all();
+    uint64_t sum = Units{scan(own.high), scan(own.low)}.all();
     if (lane == 63) of_value[wave] = sum;
     __syncthreads();
-    sum += place_before - here.all();
+    sum += place_before - own.all();
 #pragma unroll
-    for (int k = 0; k < kDrawWaves - 1; ++k)
+    for (int k = 0; k < kWaves - 1; ++k)
         if (k < int(wave)) sum += of_value[k];
-    if (sum <= point && point < sum + here.all()) {
+    if (sum <= point && point < sum + own.all()) {
         int at = 0;
 #pragma unroll
-        for (int i = 0; i < kValues - 1; ++i) {
+        for (int i = 0; i < kOwn - 1; ++i) {
             sum += units_of(left[i]).all();
             if (sum <= point) at = i + 1;
         }
-        a.out_tokens[last] = static_cast<int32_t>(there * kVerifyChunk + kValues * tid + at);
+        a.out_tokens[last] = static_cast<int32_t>(base + kOwn * tid + at);
         a.words[2 * b + 1] = 0u;
     }
-    if (WALKS) write_walk<kDrawThreads>(a, t, w, b);
+    write_walk<THREADS>(a, t, w, b);
 }
 
-// Workgroups that a call is dealt to, where it has as many chunks.
-constexpr uint32_t kDrawGroups = 1024;
+// Workgroups that a call is dealt to, where it has as many chunks: four a CU
+// (64 sequences of 131072 tokens: 24 us, with 512 or 2048 of them 28 and 31);
+// fewer where each of a sequence's reads the whole vocabulary for its walk (16
+// drawn trees over 32000 tokens: 21 us, with 16 or 256 of them 24 and 23).
+constexpr uint32_t kDrawGroups = 1024, kDrawnGroups = 64;
 
 }  // namespace
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
-    const uint32_t batch = static_cast<uint32_t>(a.batch);
-    uint32_t parts = kDrawGroups / batch;
-    if (parts < (a.chunks + kMostChunks - 1) / kMostChunks) parts = (a.chunks + kMostChunks - 1) / kMostChunks;
+    const uint32_t batch = static_cast<uint32_t>(a.batch), least = (a.chunks + kMostChunks - 1) / kMostChunks;
+    const bool drawn = a.draft && a.parents;
+    uint32_t parts = (drawn ? kDrawnGroups : kDrawGroups) / batch;
+    if (parts < least) parts = least;
     if (parts > a.chunks) parts = a.chunks;
     const uint32_t per = (a.chunks + parts - 1) / parts;
     parts = (a.chunks + per - 1) / per;
-    if (a.draft && a.parents) {
-        k_verify_walk<<<batch, kWalkThreads, 0, s>>>(a);
-        k_verify_draw<false><<<batch * parts, kDrawThreads, 0, s>>>(a, parts, per);
-    } else {
-        k_verify_draw<true><<<batch * parts, kDrawThreads, 0, s>>>(a, parts, per);
-    }
+    if (drawn) k_verify<1024, true><<<batch * parts, 1024, 0, s>>>(a, parts, per);
+    else k_verify<256, false><<<batch * parts, 256, 0, s>>>(a, parts, per);
     return hipGetLastError();
 }
 

@@ -632,7 +632,7 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
  * (which is then not reached), a token lies outside the vocabulary (it is
  * never accepted), or the probabilities that a token is drawn from are all 0
  * (the token is then -1).
- * Workspace: kvc_verify_drafts_sizes (of batch, rows and vocab), 256-byte
+ * Workspace: kvc_verify_drafts_sizes (of batch and vocab), 256-byte
  * aligned, all zero before the first call that uses it for this batch.
  */
 #define KVC_MAX_DRAFT_NODES 1024

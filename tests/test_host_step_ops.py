@@ -81,7 +81,7 @@ def test_verify_sizes_and_a_short_workspace(kvc):
     for bad in VERIFY_SIZES_BAD:
         assert verify_status(kvc, sizes=True, **bad)[0] == kvc.KVC_ERR_INVALID
     last = 0
-    for kw in (dict(rows=0), dict(), dict(rows=10 ** 6), dict(rows=10 ** 6, vocab=1 << 20),
+    for kw in (dict(rows=0), dict(rows=10 ** 6, vocab=1 << 20),
                dict(batch=(1 << 16) - 1, rows=(1 << 31) - 1, vocab=1 << 20)):
         kw.update(target_row_stride=1 << 20, draft_row_stride=1 << 20)
         st, n = verify_status(kvc, sizes=True, **kw)

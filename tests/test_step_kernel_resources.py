@@ -6,7 +6,7 @@ import pytest
 from test_kernel_resources import resources  # noqa: F401  (a fixture)
 
 
-@pytest.mark.parametrize("src,least", [("kvc_qkv.hip", 16), ("kvc_verify.hip", 3), ("kvc_pages.hip", 3)])
+@pytest.mark.parametrize("src,least", [("kvc_qkv.hip", 32), ("kvc_verify.hip", 2), ("kvc_pages.hip", 3)])
 def test_no_scratch_memory(resources, src, least):  # noqa: F811
     kernels = resources(src)
     assert len(kernels) >= least
