@@ -278,7 +278,8 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(SharedArgs a, uint32_t ta
     }
     if (!last_to_arrive(a, &order)) return;
     const int32_t count = *a.free_in;
-    for (int64_t b = tid; b < a.g.batch; b += kForkThreads) a.held_out[b] = a.held_in[b];
+    if (a.held_out != a.held_in)
+        for (int64_t b = tid; b < a.g.batch; b += kForkThreads) a.held_out[b] = a.held_in[b];
     __syncthreads();
     if (!status)
         for (int k = tid; k < a.count; k += kForkThreads)
@@ -404,7 +405,8 @@ __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     }
     if (wrong) atomicOr(&a.ctl->pending, kPagedInvalid);
     if (!last_to_arrive(a, &order)) return;
-    for (int64_t b = tid; b < a.g.batch; b += kReleaseThreads) a.held_out[b] = a.held_in[b];
+    if (a.held_out != a.held_in)
+        for (int64_t b = tid; b < a.g.batch; b += kReleaseThreads) a.held_out[b] = a.held_in[b];
     __syncthreads();
     if (sound && tid < a.count) {
         const int32_t row = a.children[tid];

@@ -185,6 +185,41 @@ def test_values_of_bf16_pages_keep_every_bit(kvc, cuda):
     assert torch.equal(bits(c.pools[1]).view(-1, 1, 128)[:rows], bits(c.v))
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.07, 3.0, 1e-30, 1e30, 2.0 ** -126, 3e38, 1e-42, 448.0, 1.0 / 3.0])
+def test_values_of_e4m3_pages_are_the_appends(kvc, cuda, scale):
+    """... and rounded to an e4m3 cache, for every pattern, as the append
+    rounds them, to the bit (a NaN's sign aside)."""
+    rows = 512
+    c = Case(kvc, cuda, rows, 1, 1, 128, 16, "e4m3", 0, False, None, False, 14)
+    c.v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(rows, 1, 128).to(cuda)
+    slots = torch.arange(rows, device=cuda)
+    plain = [p.clone() for p in c.pools]
+    kvc.PagedQKV(c.paged, 1, k_scale=scale, v_scale=scale)(0, c.q, c.v, c.v, slots)
+    kvc.kvc_paged_append(kvc.PagedKV(plain, c.paged.block_table, 16), 0, c.v, c.v, slots, k_scale=scale, v_scale=scale)
+    for x, y in zip(c.pools, plain):
+        x, y = bits(x), bits(y)
+        nan = (y & 0x7F) == 0x7F
+        assert torch.equal((x & 0x7F) == 0x7F, nan) and torch.equal(x[~nan], y[~nan])
+
+
+def test_more_rows_than_a_launch_has_waves(kvc, cuda):
+    """Waves that take several rows: as the rows by themselves."""
+    rows = 150001
+    q, k, v = (torch.randn((rows, n, 64), device=cuda).to(torch.bfloat16) for n in (5, 1, 1))
+    pos = torch.randint(-1, 5000, (rows,), device=cuda, dtype=torch.int32)
+    freq = 10000.0 ** (-torch.arange(32, dtype=torch.float64, device=cuda) / 32)
+    slots = torch.randperm(rows + 15, device=cuda)[:rows]
+    got = []
+    for step in (rows, 1 << 14):
+        pools = [torch.zeros((-(-(rows + 15) // 16), 16, 1, 64), dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+        op = kvc.PagedQKV(kvc.PagedKV(pools, torch.zeros((1, 1), dtype=torch.int32, device=cuda), 16), 5, freq)
+        out = torch.zeros_like(q)
+        for i in range(0, rows, step):
+            op(0, q[i:i + step], k[i:i + step], v[i:i + step], slots[i:i + step], pos[i:i + step], out=out[i:i + step])
+        got.append((out, *pools))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
 def test_two_streams_and_a_graph(kvc, cuda):
     """Calls on two streams through one object, and a captured one replayed on
     new rows, equal those of the current stream."""
