@@ -18,7 +18,10 @@ constexpr int kAtOnce = 8;                      // rows that a thread reads befo
 
 // A thread has 16 bytes of a sequence's rows in one pool and moves them row
 // after row: row j goes to place j from a place at or behind it, and places
-// rise, so that what is written was read before by the same thread.
+// rise, so that what is written was read before by the same thread.  Every
+// workgroup checks its sequence and finds its moves for itself, 64 at a time.
+// Bound by HBM (128 trees, 36 layers, 114 MB: 24.4 us, 4.7 TB/s), for small
+// batches by five trips to memory (4.1 us on the GPU).
 __global__ __launch_bounds__(kCompactThreads) void k_compact(CompactArgs a, uint32_t blocks) {
     __shared__ int64_t from[64], to[64];        // slots; from -1: stays
     __shared__ uint32_t moves;
@@ -221,7 +224,7 @@ __device__ uint32_t plan_fork(const SharedArgs& a, ForkPlan& p) {
 // as long as a kernel of its own would take) and takes work items in turn:
 // for each child `tables` slices of its row of the table (a parent's pages get
 // all their new holders at once, from one of its children: 256 children of 32
-// prompts 15.7 -> 10.9 us) and `copies` of the tokens of its unfilled page.  The last
+// prompts 15.7 -> 11.2 us) and `copies` of the tokens of its unfilled page.  The last
 // workgroup to be done enters the new state, which the others may still have
 // to read.
 __global__ __launch_bounds__(kForkThreads) void k_fork(SharedArgs a, uint32_t tables, uint32_t copies) {
