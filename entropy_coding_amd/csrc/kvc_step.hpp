@@ -42,7 +42,9 @@ constexpr int kVerifyChunk = 4096;      // values of a distribution that a workg
 
 // Head of the workspace; behind it two words a sequence (what the walk and
 // the draw found wrong), the workgroups of a sequence that are done (0 before
-// the first call and between calls) and the chunks' sums.
+// the first call and between calls), the chunks' sums, and of drawn trees the
+// nodes whose first rejections are summed ahead and these sums, a workgroup's
+// each.
 struct VerifyControl {
     uint32_t magic;
     uint32_t batch;
@@ -51,9 +53,23 @@ struct VerifySums {                     // units of 2^-42
     uint64_t left, whole;               // after the rejections, and before
 };
 struct VerifyLayout {
-    uint64_t words, arrived, sums, total;
+    uint64_t words, arrived, sums, first_nodes, first_sums, total;
     uint32_t chunks;
 };
+constexpr int kFirsts = 8;              // nodes of a sequence that are summed ahead
+constexpr uint32_t kMostChunks = 64;    // of a workgroup
+// Workgroups of a launch, where it has as many chunks: four a CU (64 sequences
+// of 131072 tokens: 24 us, with 512 or 2048 of them 28 and 31).
+constexpr uint32_t kDrawGroups = 1024;
+// The workgroups of a sequence, and the chunks of each.
+inline uint32_t verify_parts(uint32_t groups, uint32_t batch, uint32_t chunks, uint32_t* per) {
+    const uint32_t least = (chunks + kMostChunks - 1) / kMostChunks;
+    uint32_t parts = groups / batch;
+    if (parts < least) parts = least;
+    if (parts > chunks) parts = chunks;
+    *per = (chunks + parts - 1) / parts;
+    return (chunks + *per - 1) / *per;
+}
 inline VerifyLayout verify_layout(int64_t batch, int64_t vocab) {
     const auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
     VerifyLayout l;
@@ -61,7 +77,10 @@ inline VerifyLayout verify_layout(int64_t batch, int64_t vocab) {
     l.words = 256;
     l.arrived = l.words + up(8 * uint64_t(batch));
     l.sums = l.arrived + up(4 * uint64_t(batch));
-    l.total = l.sums + up(sizeof(VerifySums) * uint64_t(batch) * l.chunks);
+    l.first_nodes = l.sums + up(sizeof(VerifySums) * uint64_t(batch) * l.chunks);
+    l.first_sums = l.first_nodes + up(4 * kFirsts * uint64_t(batch));
+    uint32_t per;
+    l.total = l.first_sums + up(8 * kFirsts * uint64_t(batch) * verify_parts(kDrawGroups, static_cast<uint32_t>(batch), l.chunks, &per));
     return l;
 }
 struct VerifyArgs {
@@ -82,8 +101,11 @@ struct VerifyArgs {
     uint32_t* words;
     uint32_t* arrived;
     VerifySums* sums;
+    int32_t* first_nodes;
+    uint64_t* first_sums;
+    uint32_t first_parts;               // sums of a node, 0: none (the launch sets it)
 };
-hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
+hipError_t launch_verify(const VerifyArgs& args, hipStream_t s);
 
 // ---- pages
 

@@ -196,6 +196,9 @@ int kvc_verify_drafts(const kvc_drafts* p, void* d_workspace, uint64_t workspace
     a.words = reinterpret_cast<uint32_t*>(ws + l.words);
     a.arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
     a.sums = reinterpret_cast<kvc::VerifySums*>(ws + l.sums);
+    a.first_nodes = reinterpret_cast<int32_t*>(ws + l.first_nodes);
+    a.first_sums = reinterpret_cast<uint64_t*>(ws + l.first_sums);
+    a.first_parts = 0;
     return kvc::launch_verify(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KVC_OK : KVC_ERR_DEVICE;
 }
 

@@ -217,7 +217,6 @@ __device__ void write_walk(const VerifyArgs& a, const Tree& t, const Walk& w, in
 
 // ---- the draw
 
-constexpr int kMostChunks = 64;                 // of a workgroup
 
 // The distribution that a sequence draws from.
 struct Draw {
@@ -262,15 +261,77 @@ __device__ uint64_t scan_wide(uint64_t x) {
     return (uint64_t(high) << 42) + (uint64_t(mid) << 21) + low;
 }
 
+// ---- first rejections
+
+// A drawn tree's nodes whose first child would be rejected and that have
+// another: what that rejection leaves is needed there, should the walk come by,
+// and depends on no other node.  (Of a node whose first child is accepted, only
+// that one can be reached.)  All of them are summed over the vocabulary by as
+// many workgroups as the chip takes, so that the walk, which has one CU, need
+// not: 8 trees over 131072 tokens 50 -> 28 us.  Nodes behind the 64th and
+// more than kFirsts of them are left to the walk.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void k_verify_first(VerifyArgs a, uint32_t parts, uint32_t per) {
+    constexpr int kValues = 16;
+    __shared__ int32_t firsts[kFirsts];
+    __shared__ int32_t found;
+    __shared__ uint64_t of_wave[THREADS / 64];
+    const uint32_t b = blockIdx.x / parts, part = blockIdx.x - b * parts;
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const Tree t = tree_of(a, b);
+    if (tid < 64) {
+        int count = 0;
+        if (t.n) {
+            const Node x = node_of(a, t, lane);
+            const uint64_t accepted = __ballot(double(x.u) * double(x.q) < double(x.p));
+            uint64_t reached = 1, done = 0;
+            while (const uint64_t left = reached & ~done) {
+                const int v = __builtin_ctzll(left);
+                done |= uint64_t(1) << v;
+                const uint64_t children = __ballot(x.parent == v), first = children & -children;
+                if (!children) continue;
+                if (first & accepted) {
+                    reached |= first;
+                } else if (children != first) {
+                    reached |= children ^ first;
+                    if (count < kFirsts && lane == 0) firsts[count] = v;
+                    count += count < kFirsts;
+                }
+            }
+        }
+        if (lane == 0) found = count;
+    }
+    __syncthreads();
+    const int count = found;
+    if (part == 0 && tid < uint32_t(kFirsts)) a.first_nodes[b * kFirsts + tid] = int(tid) < count ? firsts[tid] : -1;
+    const uint32_t begin = part * per * kVerifyChunk, past = begin + per * kVerifyChunk;
+    const uint32_t end = past < a.vocab ? past : a.vocab;
+    const auto in_turn = [&](int g) { return 4 * (THREADS * g + tid); };
+    for (int k = 0; k < count; ++k) {
+        const Draw here{t.start + firsts[k], 1, nullptr, nullptr};
+        Units sum{0, 0};
+        for (uint32_t base = begin; base < end; base += kValues * THREADS) {
+            float x[kValues], left[kValues];
+            values_of<THREADS>(a, here, base, end, in_turn, x, left);
+#pragma unroll
+            for (int i = 0; i < kValues; ++i) sum.add(units_of(left[i]));
+        }
+        const uint64_t z = block_sum<THREADS>(sum, of_wave);
+        if (tid == 0) a.first_sums[(uint64_t(b) * kFirsts + k) * parts + part] = z;
+    }
+}
+
+// ---- walk, sums and draw
+
 // Chunks of one sequence's distribution, `per` at a time, are summed by a
 // workgroup; the last workgroup of a sequence to be done draws the token.
 // Every workgroup walks the tree for itself: chains, and trees without
 // probabilities, by its first wave, a chain of trips to memory as long as a
 // kernel of its own would take, and a launch less.  Of trees whose nodes were
-// drawn from the draft's probabilities (DRAWN) what the rejections left is
-// summed over the vocabulary before a sibling of a rejected node is tested, by
-// the whole workgroup; with 1024 threads that is bound by what one CU reads
-// (4.6 us for 32000 tokens).
+// drawn from the draft's probabilities (DRAWN) the sum of what the rejections
+// left is needed before a sibling of a rejected node is tested: a first
+// rejection's may be there (k_verify_first), others are formed by the whole
+// workgroup, bound by what one CU reads (4.6 us for 32000 tokens).
 template <int THREADS, bool DRAWN>
 __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts, uint32_t per) {
     constexpr int kWaves = THREADS / 64, kValues = 16;      // of a thread, asked for together
@@ -292,7 +353,27 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
     }
     const auto in_turn = [&](int g) { return 4 * (THREADS * g + tid); };
     if (DRAWN) {
+        const auto known_scale = [&](uint64_t z, int rejected) {
+            const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
+            if (tid == 0) w.scales[rejected] = s;
+            __syncthreads();
+            return s;
+        };
         const auto scale = [&](int current, int rejected) {
+            uint64_t z = 0;
+            int known = -1;
+            if (rejected == 1 && a.first_parts)
+                for (int k = 0; k < kFirsts; ++k)
+                    if (a.first_nodes[b * kFirsts + k] == current) known = k;
+            if (known >= 0) {
+                const uint64_t* const from = a.first_sums + (uint64_t(b) * kFirsts + known) * a.first_parts;
+                const uint64_t sum = scan_wide(tid < a.first_parts ? from[tid] : 0);
+                if (lane == 63) of_wave[0][wave] = sum;
+                __syncthreads();
+                for (int k = 0; k < kWaves; ++k) z += of_wave[0][k];
+                __syncthreads();
+                return known_scale(z, rejected);
+            }
             const Draw here{t.start + current, rejected, w.scales, nullptr};
             Units sum{0, 0};
             for (uint32_t base = 0; base < a.vocab; base += kValues * THREADS) {
@@ -301,11 +382,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
 #pragma unroll
                 for (int i = 0; i < kValues; ++i) sum.add(units_of(left[i]));
             }
-            const uint64_t z = block_sum<THREADS>(sum, of_wave[0]);
-            const float s = z ? static_cast<float>(0x1p42 / static_cast<double>(z)) : 0.0f;
-            if (tid == 0) w.scales[rejected] = s;
-            __syncthreads();
-            return s;
+            return known_scale(block_sum<THREADS>(sum, of_wave[0]), rejected);
         };
         walk(a, t, w, tid == 0, scale, [] { __syncthreads(); });
     } else if (wave == 0) {
@@ -436,24 +513,31 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
     write_walk<THREADS>(a, t, w, b);
 }
 
-// Workgroups that a call is dealt to, where it has as many chunks: four a CU
-// (64 sequences of 131072 tokens: 24 us, with 512 or 2048 of them 28 and 31);
-// fewer where each of a sequence's reads the whole vocabulary for its walk (16
-// drawn trees over 32000 tokens: 21 us, with 16 or 256 of them 24 and 23).
-constexpr uint32_t kDrawGroups = 1024, kDrawnGroups = 64;
+// Workgroups of 1024 threads for drawn trees, each of which may read a whole
+// vocabulary for its walk: fewer than the chip holds, and fewest where that is
+// short (16 trees over 32000 tokens: 21 us, with 16 or 256 of them 24 and 23).
+constexpr uint32_t kDrawnGroups = 64, kDrawnGroupsWide = 256;
+// From this many chunks on, first rejections are summed ahead: another launch
+// (1 tree over 32000 tokens 12.4 -> 14.4 us, 200 of them 33 -> 43) that saves a
+// CU's pass over a wide vocabulary (131072 tokens, 1 tree 15.2 -> 14.3 us, 8
+// trees 50 -> 28, 64 of 8 nodes 62 -> 54).
+constexpr uint32_t kFirstChunks = 16;
 
 }  // namespace
 
-hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
-    const uint32_t batch = static_cast<uint32_t>(a.batch), least = (a.chunks + kMostChunks - 1) / kMostChunks;
-    const bool drawn = a.draft && a.parents;
-    uint32_t parts = (drawn ? kDrawnGroups : kDrawGroups) / batch;
-    if (parts < least) parts = least;
-    if (parts > a.chunks) parts = a.chunks;
-    const uint32_t per = (a.chunks + parts - 1) / parts;
-    parts = (a.chunks + per - 1) / per;
-    if (drawn) k_verify<1024, true><<<batch * parts, 1024, 0, s>>>(a, parts, per);
-    else k_verify<256, false><<<batch * parts, 256, 0, s>>>(a, parts, per);
+hipError_t launch_verify(const VerifyArgs& args, hipStream_t s) {
+    VerifyArgs a = args;
+    const uint32_t batch = static_cast<uint32_t>(a.batch);
+    uint32_t per, parts = verify_parts(kDrawGroups, batch, a.chunks, &per);
+    if (!a.draft || !a.parents) {
+        k_verify<256, false><<<batch * parts, 256, 0, s>>>(a, parts, per);
+        return hipGetLastError();
+    }
+    const bool wide = a.chunks >= kFirstChunks;
+    a.first_parts = wide ? parts : 0;
+    if (wide) k_verify_first<256><<<batch * parts, 256, 0, s>>>(a, parts, per);
+    parts = verify_parts(wide ? kDrawnGroupsWide : kDrawnGroups, batch, a.chunks, &per);
+    k_verify<1024, true><<<batch * parts, 1024, 0, s>>>(a, parts, per);
     return hipGetLastError();
 }
 

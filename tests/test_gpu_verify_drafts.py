@@ -243,6 +243,18 @@ def test_tokens_follow_the_target(kvc, cuda, mode):
             follows(second, p[node])
 
 
+@pytest.mark.parametrize("vocab", [65536, 61441, 100003])
+@pytest.mark.parametrize("wide,noise", [(3, 0.5), (1000, 0.5), (4, 3.0)])
+def test_drawn_trees_over_wide_vocabularies(kvc, cuda, vocab, wide, noise):
+    """First rejections summed ahead: of deep trees, of stars with more
+    children than are summed ahead for, of drafts that are rejected often, of
+    more nodes than are looked at."""
+    c = Case([9, 1, 0, 24, 70], vocab, True, wide, vocab + wide, pad=1, sharp=noise + 1)
+    rng = np.random.default_rng(1)
+    c.accept[:] = rng.random(len(c.accept), dtype=np.float32) ** np.float32(1 / noise)
+    c.run(kvc, cuda)
+
+
 def test_results_do_not_change_from_call_to_call(kvc, cuda):
     c = Case([9] * 40, 9000, True, 3, 18)
     v = kvc.DraftVerifier(40, 9000, 360)
