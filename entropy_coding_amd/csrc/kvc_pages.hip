@@ -78,7 +78,8 @@ __global__ __launch_bounds__(kCompactThreads) void k_compact(CompactArgs a, uint
         __syncthreads();
         const uint32_t count = moves;
         for (uint64_t i = uint64_t(block) * kCompactThreads + tid; i < all; i += uint64_t(blocks) * kCompactThreads) {
-            const uint32_t pool = static_cast<uint32_t>(i / a.g.pieces), piece = static_cast<uint32_t>(i - uint64_t(pool) * a.g.pieces);
+            const uint32_t pool = static_cast<uint32_t>(all >> 32 ? i / a.g.pieces : static_cast<uint32_t>(i) / a.g.pieces);
+            const uint32_t piece = static_cast<uint32_t>(i - uint64_t(pool) * a.g.pieces);
             u32x4* const base = static_cast<u32x4*>(a.g.pools[pool]) + piece;
             for (uint32_t m = 0; m < count; m += kAtOnce) {
                 u32x4 x[kAtOnce];
@@ -224,9 +225,9 @@ __device__ uint32_t plan_fork(const SharedArgs& a, ForkPlan& p) {
 // as long as a kernel of its own would take) and takes work items in turn:
 // for each child `tables` slices of its row of the table (a parent's pages get
 // all their new holders at once, from one of its children: 256 children of 32
-// prompts 15.7 -> 11.2 us) and `copies` of the tokens of its unfilled page.  The last
-// workgroup to be done enters the new state, which the others may still have
-// to read.
+// prompts 15.7 -> 11.2 us) and `copies` of the tokens of its unfilled page.
+// The last workgroup to be done enters the new state, which the others may
+// still have to read.
 __global__ __launch_bounds__(kForkThreads) void k_fork(SharedArgs a, uint32_t tables, uint32_t copies) {
     __shared__ ForkPlan p;
     __shared__ uint32_t order;
@@ -308,8 +309,8 @@ constexpr int kMerged = 2048;
 // and takes a page's holders off at once: they are counted in LDS, in a place
 // by the page's hash (a page whose place is another's is counted down by
 // itself; four columns 15.5 us for 256 requests of 8 prompts, sixteen 16.8).
-// The last workgroup to be done pushes the marked pages in the order
-// of their numbers, clears marks and counts and enters the new state.
+// The last workgroup to be done pushes the marked pages in the order of their
+// numbers, clears marks and counts and enters the new state.
 __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     __shared__ int32_t requests[kMaxShared], held_by[kMaxShared];
     __shared__ int32_t pages[kMerged], holders[kMerged];

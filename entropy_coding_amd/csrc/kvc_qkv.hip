@@ -80,14 +80,15 @@ __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
 // has groups of lanes; UNIFORM: all of a step's heads are of one kind.  The
 // next step's values are asked for before this one's are looked at, a row's
 // first ones before its position.  An angle's sine and cosine are formed once
-// a row, one in a lane, and handed round through LDS.  Bound by HBM where rows
-// are many (16384 of 32 and 16 heads of 128 bf16 channels, 403 MB: 82 us, as
-// long as a copy of as many bytes; vector instructions 38% of the cycles), by
-// a wave's trips to memory where they are few (4 rows: 4.1 us on the GPU), by
-// a short launch's start and end between (5003 rows to e4m3, 101 MB: 29 us, a
-// copy's rate gives 21).
+// a row, one in a lane, and read from LDS for every head (kept in registers
+// they left four waves a SIMD instead of five: 82 -> 80 us and 29 -> 27 us for
+// the calls named here).  Bound by HBM where rows are many (16384 of 32 and 16
+// heads of 128 bf16 channels, 403 MB: 80 us, a copy of as many bytes 82; vector
+// instructions 38% of the cycles), by a wave's trips to memory where they are
+// few (4 rows: 4.0 us on the GPU), by a short launch's start and end between
+// (5003 rows to e4m3, 101 MB: 27 us, a copy's rate gives 21).
 template <int D, bool FP8, bool NEIGHBOURS, bool UNIFORM>
-__global__ __launch_bounds__(64 * kQkvWaves, 4) void k_qkv(QkvArgs a) {
+__global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
     constexpr int kUnits = D / 16;              // lanes that a head needs
     constexpr int kGroup = kUnits == 12 ? 16 : kUnits;
     constexpr int kHeads = 64 / kGroup;
@@ -136,9 +137,9 @@ __global__ __launch_bounds__(64 * kQkvWaves, 4) void k_qkv(QkvArgs a) {
         const int32_t position = a.positions ? a.positions[row] : 0;
         if (position < 0) continue;
         const int64_t slot = a.slots[row];
-        float c[8], s[8];
         if (a.rotary) {
             // Whole turns are taken off in 64 bits, so that far positions are as exact as near ones.
+            __builtin_amdgcn_wave_barrier();    // (the last row's are read)
             for (uint32_t i = lane; i < half; i += 64) {
                 double t = double(position) * (a.frequencies[i] * 0.15915494309189535);
                 t -= rint(t);
@@ -149,12 +150,6 @@ __global__ __launch_bounds__(64 * kQkvWaves, 4) void k_qkv(QkvArgs a) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 t = turns[wave][turned ? 8 * u + i : 0];
-                c[i] = t.x;
-                s[i] = t.y;
-            }
             __builtin_amdgcn_wave_barrier();
         }
         for (uint32_t step = begin; step < end; ++step) {
@@ -214,7 +209,8 @@ __global__ __launch_bounds__(64 * kQkvWaves, 4) void k_qkv(QkvArgs a) {
                 for (int i = 0; i < 8; ++i) {
                     float& left = NEIGHBOURS ? x[i / 4][2 * (i % 4)] : x[0][i];
                     float& right = NEIGHBOURS ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
-                    const float l = fmaf(left, c[i], -(right * s[i])), y = fmaf(left, s[i], right * c[i]);
+                    const float2 t = turns[wave][8 * u + i];
+                    const float l = fmaf(left, t.x, -(right * t.y)), y = fmaf(left, t.y, right * t.x);
                     left = l;
                     right = y;
                 }
@@ -259,8 +255,8 @@ hipError_t launch(const QkvArgs& args, hipStream_t s) {
     QkvArgs a = args;
     constexpr int kHeads = 64 / (D == 192 ? 16 : D / 16);
     const int64_t steps = (int64_t(a.q_heads) + 2 * int64_t(a.heads) + kHeads - 1) / kHeads;
-    // Few rows: a wave a step.  Else two waves a row: one leaves the chip's 4096 waves unevenly filled (5003 rows to
-    // e4m3: 33 us against 29; 16384 rows alike), three form the angles too often (30 us, and 85 us against 83).
+    // Few rows: a wave a step.  Else two waves a row (16384 rows 80 us, 5003 rows to e4m3 26.5 us; one wave 86 and
+    // 27.4 us, the chip being filled unevenly; three, which form the angles once more, 82 and 27.1).
     a.parts = a.rows * steps <= 4096 ? static_cast<uint32_t>(steps) : steps > 2 ? 2 : 1;
     int64_t blocks = (a.rows * a.parts + kQkvWaves - 1) / kQkvWaves;
     if (blocks > 1 << 16) blocks = 1 << 16;

@@ -625,7 +625,8 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
  * as 0; rows of probabilities are taken to sum to 1.  Random numbers lie in
  * [0, 1).
  * vocab and batch at most 2^20, batch x ceil(vocab / 4096) < 2^24; a row
- * stride (in values, at least vocab) between one row is not looked at.  Does not synchronise.
+ * stride (in values, at least vocab) between one row is not looked at.  Does
+ * not synchronise.
  * kvc_verify_drafts_result gives KVC_ERR_INVALID where a sequence's row starts
  * fall or pass `rows` or it has too many nodes (its kept length is then 0 and
  * nothing else of it written), where a parent does not come before its node
@@ -723,14 +724,14 @@ int kvc_paged_compact_result(const void* d_workspace, void* stream);
  *
  * kvc_release_pages: the requests d_requests[k], k < count (-1: none), are
  * finished: each page that they hold loses a holder (d_extra goes down by
- * one); pages that had no further holder go to the stack, in ascending order,
- * the highest on top; their d_extra is 0; the requests hold none.
+ * one); pages that no request holds any more go to the stack, in ascending
+ * order, the highest on top; their d_extra is 0; the requests hold none.
  * KVC_ERR_INVALID for a request outside the batch, a held count outside [0,
  * max_pages] (both left alone), a request that stands twice (released once),
  * a page number outside the pools (passed over), a page that loses more
  * holders than it has (given back once), or a *d_free_in outside [0,
  * free_capacity] (nothing is done); KVC_ERR_CAPACITY where the stack would
- * pass free_capacity (pages of several entries of it: what fits is pushed).
+ * pass free_capacity, as one that holds a page twice may (what fits is pushed).
  *
  * A request whose pages were shared is finished with kvc_release_pages, not
  * with a trim, and not trimmed below the tokens that it was forked from or
