@@ -82,11 +82,13 @@ __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
 // first ones before its position.  An angle's sine and cosine are formed once
 // a row, one in a lane, and read from LDS for every head (kept in registers
 // they left four waves a SIMD instead of five: 82 -> 80 us and 29 -> 27 us for
-// the calls named here).  Bound by HBM where rows are many (16384 of 32 and 16
-// heads of 128 bf16 channels, 403 MB: 80 us, a copy of as many bytes 82; vector
-// instructions 38% of the cycles), by a wave's trips to memory where they are
-// few (4 rows: 4.0 us on the GPU), by a short launch's start and end between
-// (5003 rows to e4m3, 101 MB: 27 us, a copy's rate gives 21).
+// the calls named here).  Stores are not kept in the caches (80 -> 75 us, 27 ->
+// 23 us; an attention behind them takes as long as before).  Bound by HBM where
+// rows are many (16384 of 32 and 16 heads of 128 bf16 channels, 403 MB: 75 us,
+// 5.4 TB/s; a copy of as many bytes 82; vector instructions 41% of the cycles),
+// by a wave's trips to memory where they are few (4 rows: 4.0 us on the GPU),
+// by a short launch's start and end between (5003 rows to e4m3, 101 MB: 23 us,
+// a copy's rate gives 21).
 template <int D, bool FP8, bool NEIGHBOURS, bool UNIFORM>
 __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
     constexpr int kUnits = D / 16;              // lanes that a head needs
@@ -231,10 +233,10 @@ __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
                     y[i] = round_scaled(four[0], four[1], per_scale) | (round_scaled(four[2], four[3], per_scale) << 16);
                 }
                 if (apart) {
-                    *(Global<u32x2>*)(to + first) = u32x2{y[0], y[1]};
-                    *(Global<u32x2>*)(to + second) = u32x2{y[2], y[3]};
+                    __builtin_nontemporal_store(u32x2{y[0], y[1]}, (Global<u32x2>*)(to + first));
+                    __builtin_nontemporal_store(u32x2{y[2], y[3]}, (Global<u32x2>*)(to + second));
                 } else {
-                    *(Global<u32x4>*)(to + first) = y;
+                    __builtin_nontemporal_store(y, (Global<u32x4>*)(to + first));
                 }
             } else {
 #pragma unroll
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
                     if (t.kind != kValue)
                         y = u32x4{two_bf16(x[p][0], x[p][1]), two_bf16(x[p][2], x[p][3]),
                                   two_bf16(x[p][4], x[p][5]), two_bf16(x[p][6], x[p][7])};
-                    *(Global<u32x4>*)(to + 2 * (p ? second : first)) = y;
+                    __builtin_nontemporal_store(y, (Global<u32x4>*)(to + 2 * (p ? second : first)));
                 }
             }
         }
@@ -255,8 +257,9 @@ hipError_t launch(const QkvArgs& args, hipStream_t s) {
     QkvArgs a = args;
     constexpr int kHeads = 64 / (D == 192 ? 16 : D / 16);
     const int64_t steps = (int64_t(a.q_heads) + 2 * int64_t(a.heads) + kHeads - 1) / kHeads;
-    // Few rows: a wave a step.  Else two waves a row (16384 rows 80 us, 5003 rows to e4m3 26.5 us; one wave 86 and
-    // 27.4 us, the chip being filled unevenly; three, which form the angles once more, 82 and 27.1).
+    // Few rows: a wave a step.  Else two waves a row (before stores passed the caches: 16384 rows 80 us, 5003 rows to
+    // e4m3 26.5 us; one wave 86 and 27.4 us, the chip being filled unevenly; three, which form the angles once more, 82
+    // and 27.1).
     a.parts = a.rows * steps <= 4096 ? static_cast<uint32_t>(steps) : steps > 2 ? 2 : 1;
     int64_t blocks = (a.rows * a.parts + kQkvWaves - 1) / kQkvWaves;
     if (blocks > 1 << 16) blocks = 1 << 16;
