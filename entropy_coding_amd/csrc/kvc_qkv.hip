@@ -85,7 +85,7 @@ __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
 // the calls named here).  Stores are not kept in the caches (80 -> 75 us, 27 ->
 // 23 us; an attention behind them takes as long as before).  Bound by HBM where
 // rows are many (16384 of 32 and 16 heads of 128 bf16 channels, 403 MB: 75 us,
-// 5.4 TB/s; a copy of as many bytes 82; vector instructions 41% of the cycles),
+// 5.4 TB/s; a copy of as many bytes 82; vector instructions 39% of the cycles),
 // by a wave's trips to memory where they are few (4 rows: 4.0 us on the GPU),
 // by a short launch's start and end between (5003 rows to e4m3, 101 MB: 23 us,
 // a copy's rate gives 21).
