@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kCompactThreads) void k_compact(CompactArgs a, uint
         bad = __syncthreads_or(wrong);
     }
     if (block == 0 && tid == 0) {
-        if (b == 0) *a.ctl = CompactControl{kPagedMagic, static_cast<uint32_t>(a.g.batch)};
+        if (b == 0) *a.ctl = CompactControl{kCompactMagic, static_cast<uint32_t>(a.g.batch)};
         a.words[b] = bad ? kPagedInvalid : 0u;
     }
     if (bad) return;
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(SharedArgs a, uint32_t ta
     if (tid == 0) {
         *a.free_out = status ? count : count - static_cast<int32_t>(p.all);
         const uint32_t pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.ctl->magic = kPagedMagic;
+        a.ctl->magic = kSharedMagic;
         a.ctl->flags = status | pending;
     }
 }
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     if (tid == 0) {
         *a.free_out = static_cast<int32_t>(at < a.free_capacity || !sound ? at : a.free_capacity);
         const uint32_t pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.ctl->magic = kPagedMagic;
+        a.ctl->magic = kSharedMagic;
         a.ctl->flags = (sound ? 0u : kPagedInvalid) | pending | (full ? kPagedCapacity : 0u);
     }
 }

@@ -9,6 +9,9 @@
 
 namespace kvc {
 
+// Workspaces that a call of the kind has written.
+constexpr uint32_t kVerifyMagic = 0x6b766376u, kCompactMagic = 0x6b76636du, kSharedMagic = 0x6b766373u;
+
 // ---- norms, rotation, append
 
 struct HeadRows {                       // [rows][heads][channels], strides in values

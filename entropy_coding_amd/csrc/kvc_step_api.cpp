@@ -207,7 +207,7 @@ int kvc_verify_drafts_result(const void* d_workspace, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     kvc::VerifyControl c;
     if (!read_back(&c, d_workspace, sizeof(c), s)) return KVC_ERR_DEVICE;
-    if (c.magic != kvc::kPagedMagic) return KVC_ERR_INVALID;
+    if (c.magic != kvc::kVerifyMagic) return KVC_ERR_INVALID;
     return outcome_of_words(static_cast<const char*>(d_workspace) + 256, 2 * uint64_t(c.batch), s);
 }
 
@@ -239,7 +239,7 @@ int kvc_paged_compact_result(const void* d_workspace, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     kvc::CompactControl c;
     if (!read_back(&c, d_workspace, sizeof(c), s)) return KVC_ERR_DEVICE;
-    if (c.magic != kvc::kPagedMagic) return KVC_ERR_INVALID;
+    if (c.magic != kvc::kCompactMagic) return KVC_ERR_INVALID;
     return outcome_of_words(static_cast<const char*>(d_workspace) + 256, c.batch, s);
 }
 
@@ -272,7 +272,7 @@ int kvc_shared_pages_result(const void* d_workspace, void* stream) {
     if (!d_workspace || !aligned(d_workspace, 256)) return KVC_ERR_INVALID;
     kvc::SharedControl c;
     if (!read_back(&c, d_workspace, sizeof(c), static_cast<hipStream_t>(stream))) return KVC_ERR_DEVICE;
-    return c.magic == kvc::kPagedMagic ? outcome(c.flags) : KVC_ERR_INVALID;
+    return c.magic == kvc::kSharedMagic ? outcome(c.flags) : KVC_ERR_INVALID;
 }
 
 }  // extern "C"

@@ -343,7 +343,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
     __shared__ uint64_t place_before;
     const uint32_t b = blockIdx.x / parts, part = blockIdx.x - b * parts;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (blockIdx.x == 0 && tid == 0) *a.ctl = VerifyControl{kPagedMagic, static_cast<uint32_t>(a.batch)};
+    if (blockIdx.x == 0 && tid == 0) *a.ctl = VerifyControl{kVerifyMagic, static_cast<uint32_t>(a.batch)};
     const float u = a.sample[b];                // (asked for now: a trip less behind the sums)
     const Tree t = tree_of(a, b);
     if (t.n == 0) {

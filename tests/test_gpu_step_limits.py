@@ -163,3 +163,117 @@ def test_made_within_a_capture(kvc, cuda):
         v.result()
         c.check(got)
         torch.cuda.synchronize()
+
+
+def test_two_graphs_of_one_object(kvc, cuda):
+    """Captured calls that share an object's workspace, replayed in turn with
+    eager calls of it between."""
+    for draft, wide in ((True, 0), (True, 3), (False, 3)):
+        cases = [Case([7, 3, 12], 9000, draft, wide, 40 + i) for i in range(2)]
+        v = kvc.DraftVerifier(3, 9000, 22)
+        args, graphs = [c.args(cuda) for c in cases], []
+        outs = [v(**a) for a in args]
+        torch.cuda.synchronize()
+        for a, o in zip(args, outs):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                v(**a, kept=o[0], kept_lens=o[1], out_tokens=o[2])
+            graphs.append(graph)
+        for turn in range(6):
+            i = turn % 2
+            for t in outs[i]:
+                t.fill_(-7)
+            graphs[i].replay()
+            if turn % 3 == 0:
+                cases[1 - i].check(v(**args[1 - i]))
+            v.result()
+            cases[i].check(outs[i])
+
+
+def test_captured_forks_and_releases(kvc, cuda):
+    """A graph that forks and one that releases, replayed with new lists,
+    padding among them, and an eager call between."""
+    lens = np.array([40, 33, 0, 0, 0, 0, 0])
+    c = Cache(kvc, cuda, [3, 3, 0, 0, 0, 0, 0], 16, 2, 2, 64, "bf16", 50)
+    s = c.share()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda)
+    parents, children, ends, length = i32([0, 0, 0, 0]), i32([-1] * 4), i32([-1] * 4), i32(lens.tolist())
+    s.fork(parents, children, length)
+    s.release(ends)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        s.fork(parents, children, length)
+    with torch.cuda.graph(graphs[1]):
+        s.release(ends)
+    for who, what, gone in (([0, 1, 0, 0], [2, 3, -1, 4], [3, -1, 2, -1]), ([1, 4, 0, 4], [-1, 2, 3, 5], [4, 5, -1, 3]),
+                            ([1, 1, 1, 1], [3, 4, 5, 6], [6, 5, 4, 3])):
+        for p, x in zip(who, what):
+            lens[x] = lens[p] if x >= 0 else lens[x]
+        parents.copy_(i32(who))
+        children.copy_(i32(what))
+        length.copy_(i32(lens.tolist()))
+        graphs[0].replay()
+        s.result()
+        c.table, c.held, c.count, c.extra = S.fork(c.pools.numpy(), c.table, c.held, c.free, c.count, c.extra, 16, who, what, lens)
+        c.same()
+        ends.copy_(i32(gone))
+        graphs[1].replay()
+        s.result()
+        c.held, c.free, c.count, c.extra = S.release(c.table, c.held, c.free, c.count, c.extra, gone)
+        c.same()
+        for x in gone:
+            lens[x] = 0 if x >= 0 else lens[x]
+    c.release([2, 0, 1])
+    assert c.count == c.num_pages and not c.extra.any()
+
+
+def test_outcomes_of_other_workspaces(kvc, cuda):
+    """An outcome is read from a workspace that a call of its own kind has
+    written, and from no other."""
+    w = Work(kvc, cuda, 60)
+    made = w.make()
+    for op in made[:3]:
+        with pytest.raises(kvc.KvcError):
+            op.result()                          # (none has been called)
+    w.call(made)
+    for op in made[:3]:
+        op.result()
+    calls = [kvc._lib_verify_result, kvc._lib_compact_result, kvc._lib_shared_result, kvc._lib_attention_result,
+             lambda ws, s: kvc._lib_block_table_result(ws, s, None)]
+    stream = torch.cuda.current_stream().cuda_stream
+    for i, op in enumerate(made[:3]):
+        for k, call in enumerate(calls):
+            assert call(op.workspace.data_ptr(), stream) == (kvc.KVC_OK if i == k else kvc.KVC_ERR_INVALID)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(kvc, cuda, kind):
+    """Keys, values and an unfilled page at the far end of pools of more than
+    4 GiB: as in near ones."""
+    dtype, page, heads, d = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn, 16, 2, 128
+    raw = torch.int16 if kind == "bf16" else torch.uint8
+    num_pages = (5 << 30) // (page * heads * d * (2 if kind == "bf16" else 1))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda)
+    n = 23
+    q, k, v = (torch.randn((n, m, d), device=cuda).to(torch.bfloat16) for m in (4, heads, heads))
+    pos = torch.arange(n, device=cuda)
+    freq = 100.0 ** (-torch.arange(64, dtype=torch.float64, device=cuda) / 64)
+    got = []
+    for pages, row, top in ((num_pages, [num_pages - 1, num_pages - 3], num_pages - 2), (4, [3, 1], 2)):
+        pools = [torch.empty((pages, page, heads, d), dtype=dtype, device=cuda) for _ in range(2)]
+        table = i32([row, [-1, -1]])
+        paged = kvc.PagedKV(pools, table, page)
+        slots = table[0].long()[pos // page] * page + pos % page
+        out = kvc.PagedQKV(paged, 4, freq)(0, q, k, v, slots, pos.int())
+        free = torch.full((pages,), top, dtype=torch.int32, device=cuda)
+        shared = kvc.SharedPages(paged, i32([2, 0]), free, i32([1]), torch.zeros(pages, dtype=torch.int32, device=cuda))
+        shared.fork(i32([0]), i32([1]), i32([n, 0]))
+        shared.result()
+        assert table[1].tolist() == [row[0], top]
+        got.append([out] + [p.view(raw)[x, : y].clone() for p in pools for x, y in ((row[0], page), (row[1], n - page), (top, n - page))])
+        shared.release(i32([0, 1]))
+        shared.result()
+        assert shared.free_pages[:3].tolist() == sorted([*row, top])
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(got[0][2], got[0][3]) and torch.equal(got[0][5], got[0][6])
