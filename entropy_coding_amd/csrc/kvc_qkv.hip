@@ -102,7 +102,6 @@ __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
     const bool apart = turned && !NEIGHBOURS;
     const uint32_t first = apart ? 8 * u : 16 * u, second = apart ? half + 8 * u : 16 * u + 8;
     const uint32_t all = a.q_heads + 2 * a.heads, steps = (all + kHeads - 1) / kHeads;
-    const uint32_t per = (steps + a.parts - 1) / a.parts;
     const int64_t items = a.rows * a.parts;
 
     struct Step {
@@ -133,8 +132,7 @@ __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
     for (int64_t item = int64_t(blockIdx.x) * kQkvWaves + wave; item < items; item += int64_t(gridDim.x) * kQkvWaves) {
         const int64_t row = a.parts == 1 ? item : item / a.parts;
         const uint32_t part = static_cast<uint32_t>(item - row * a.parts);
-        const uint32_t begin = part * per, end = begin + per < steps ? begin + per : steps;
-        if (begin >= end) continue;
+        const uint32_t begin = part * steps / a.parts, end = (part + 1) * steps / a.parts;
         Pieces next = fetch(row, begin);
         const int32_t position = a.positions ? a.positions[row] : 0;
         if (position < 0) continue;
@@ -257,10 +255,10 @@ hipError_t launch(const QkvArgs& args, hipStream_t s) {
     QkvArgs a = args;
     constexpr int kHeads = 64 / (D == 192 ? 16 : D / 16);
     const int64_t steps = (int64_t(a.q_heads) + 2 * int64_t(a.heads) + kHeads - 1) / kHeads;
-    // Few rows: a wave a step.  Else two waves a row (before stores passed the caches: 16384 rows 80 us, 5003 rows to
-    // e4m3 26.5 us; one wave 86 and 27.4 us, the chip being filled unevenly; three, which form the angles once more, 82
-    // and 27.1).
-    a.parts = a.rows * steps <= 4096 ? static_cast<uint32_t>(steps) : steps > 2 ? 2 : 1;
+    // Few rows: a wave a step.  Else at most four steps a wave: whole rows leave the chip's waves unevenly filled where
+    // they are long (6081 rows of 64 and 8 heads of 256 channels 94 us, with two waves a row 105; two or three steps a
+    // wave take as long as four), and each part forms the row's angles.
+    a.parts = static_cast<uint32_t>(a.rows * steps <= 4096 ? steps : (steps + 3) / 4);
     int64_t blocks = (a.rows * a.parts + kQkvWaves - 1) / kQkvWaves;
     if (blocks > 1 << 16) blocks = 1 << 16;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(64 * kQkvWaves);
