@@ -136,6 +136,7 @@ struct ForkPlan {
     int32_t sharing[2 * kMaxShared];    // children of such a parent
     uint32_t of_wave[kForkThreads / 64];
     uint32_t all;                       // pages taken from the stack
+    int32_t count;                      // its height before
 };
 
 // The place of a number in a table of 2 kMaxShared, of which at most half are
@@ -217,7 +218,10 @@ __device__ uint32_t plan_fork(const SharedArgs& a, ForkPlan& p) {
         const int32_t at = p.entries[k].holders;
         p.entries[k].holders = at >= 0 && p.seen[1][at] == k ? p.sharing[at] : 0;
     }
-    if (tid == 0) p.all = taken;
+    if (tid == 0) {
+        p.all = taken;
+        p.count = static_cast<int32_t>(count);
+    }
     wrong = __syncthreads_or(wrong);
     return wrong ? kPagedInvalid : int64_t(taken) <= count ? 0u : kPagedCapacity;
 }
@@ -282,16 +286,17 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(SharedArgs a, uint32_t ta
         }
     }
     if (!last_to_arrive(a, &order)) return;
-    const int32_t count = *a.free_in;
-    if (a.held_out != a.held_in)
+    uint32_t pending = 0;                       // (asked for now, needed at the end)
+    if (tid == 0) pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (a.held_out != a.held_in) {
         for (int64_t b = tid; b < a.g.batch; b += kForkThreads) a.held_out[b] = a.held_in[b];
-    __syncthreads();
+        __syncthreads();
+    }
     if (!status)
         for (int k = tid; k < a.count; k += kForkThreads)
             if (p.entries[k].child >= 0) a.held_out[p.entries[k].child] = p.entries[k].whole + (p.entries[k].rest > 0);
     if (tid == 0) {
-        *a.free_out = status ? count : count - static_cast<int32_t>(p.all);
-        const uint32_t pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *a.free_out = status ? p.count : p.count - static_cast<int32_t>(p.all);
         a.ctl->magic = kSharedMagic;
         a.ctl->flags = status | pending;
     }
@@ -306,12 +311,14 @@ constexpr int kMerged = 2048;
 
 // Every page of the requests loses a holder; those that have none left (their
 // count passes 0) are marked, a bit a page.  A workgroup takes a few columns of
-// all the requests' rows, where those that share a prompt have the same pages,
-// and takes a page's holders off at once: they are counted in LDS, in a place
-// by the page's hash (a page whose place is another's is counted down by
-// itself; four columns 15.5 us for 256 requests of 8 prompts, sixteen 16.8).
-// The last workgroup to be done pushes the marked pages in the order of their
-// numbers, clears marks and counts and enters the new state.
+// all the requests' rows (four: 256 requests on 8 prompts 15.5 us, sixteen 16.8,
+// both before the marks lay apart), where those that share a prompt have the
+// same pages, and takes a page's holders off at once: they are counted in LDS,
+// in a place by the page's hash (a page whose place is another's is counted
+// down by itself).  The last workgroup to be done pushes the marked pages in the
+// order of their numbers, clears marks and counts and enters the new state.
+// Bound by its chain of trips to memory: requests, held counts, table, counts,
+// marks, two arrivals, marks (10.6 us, 6.7 for four requests).
 __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     __shared__ int32_t requests[kMaxShared], held_by[kMaxShared];
     __shared__ int32_t pages[kMerged], holders[kMerged];
@@ -325,6 +332,7 @@ __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     requests[tid] = row;
     if (row >= 0 && row < a.g.batch) held = a.held_in[row];
     else if (row != -1) wrong = true;
+    const bool clears = row >= 0 && row < a.g.batch && held >= 0 && held <= a.g.max_pages;
     if (held < 0 || held > a.g.max_pages) {
         wrong = true;
         held = 0;
@@ -356,7 +364,7 @@ __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     for (int w = 0; w < kReleaseThreads / 64; ++w) widest = widest > of_wave[w] ? widest : of_wave[w];
     // what a page's count is behind the holders that leave
     const auto left_by = [&](int32_t page, int32_t left) {
-        if (left < 0) atomicOr(&a.bits[page >> 5], 1u << (page & 31));
+        if (left < 0) atomicOr(&a.bits[(page >> 5) * kMarkStride], 1u << (page & 31));
         if (left < -1) wrong = true;
     };
     constexpr int kEach = kMerged / kReleaseThreads, kRounds = 4;
@@ -412,54 +420,60 @@ __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     }
     if (wrong) atomicOr(&a.ctl->pending, kPagedInvalid);
     if (!last_to_arrive(a, &order)) return;
-    if (a.held_out != a.held_in)
+    uint32_t pending = 0;                       // (asked for now, needed at the end)
+    if (tid == 0) pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (a.held_out != a.held_in) {
         for (int64_t b = tid; b < a.g.batch; b += kReleaseThreads) a.held_out[b] = a.held_in[b];
-    __syncthreads();
-    if (sound && tid < a.count) {
-        const int32_t row = a.children[tid];
-        if (row >= 0 && row < a.g.batch && a.held_out[row] >= 0 && a.held_out[row] <= a.g.max_pages) a.held_out[row] = 0;
+        __syncthreads();
     }
+    if (sound && clears) a.held_out[row] = 0;
     // 1024 words of marks at a time: their places on the stack first, then a lane a page
     int64_t at = count;
     const int64_t words = (a.g.num_pages + 31) / 32;
-    bool full = false;
     uint32_t* const marks = reinterpret_cast<uint32_t*>(pages);
     int32_t* const places = holders;
     for (int64_t w0 = 0; sound && w0 < words; w0 += kReleaseThreads) {
         const int64_t w = w0 + tid;
-        const uint32_t bits = w < words ? __hip_atomic_load(&a.bits[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+        const uint32_t bits = w < words ? __hip_atomic_load(&a.bits[w * kMarkStride], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
         const uint32_t mine = __builtin_popcount(bits), upto = scan(mine);
+        if (w0) __syncthreads();                // (the last words' are read)
         if (lane == 63) of_wave[wave] = upto;
+        marks[tid] = bits;
+        places[tid] = static_cast<int32_t>(upto - mine);    // within the wave's 64 words
         __syncthreads();
-        uint32_t before = 0, all = 0;
+        uint32_t before[kReleaseThreads / 64], all = 0;
         for (int i = 0; i < kReleaseThreads / 64; ++i) {
-            if (i < wave) before += of_wave[i];
+            before[i] = all;
             all += of_wave[i];
         }
-        marks[tid] = bits;
-        places[tid] = static_cast<int32_t>(before + upto - mine);
-        if (bits) __hip_atomic_store(&a.bits[w], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (all) {
-            const int pairs = words - w0 < kReleaseThreads ? static_cast<int>(words - w0 + 1) / 2 : kReleaseThreads / 2;
-#pragma unroll 4
-            for (int pair = wave; pair < pairs; pair += kReleaseThreads / 64) {
-                const uint32_t word = marks[2 * pair + (lane >> 5)], bit = lane & 31;
-                if (!(word >> bit & 1u)) continue;
-                const int64_t place = at + places[2 * pair + (lane >> 5)] + __builtin_popcount(word & ((1u << bit) - 1));
-                const int32_t page = static_cast<int32_t>(w0 * 32 + 64 * pair + lane);
+        const int pairs = !all ? 0 : words - w0 < kReleaseThreads ? static_cast<int>(words - w0 + 1) / 2 : kReleaseThreads / 2;
+        constexpr int kPairs = 4;               // of a wave, looked up together
+        for (int pair0 = kPairs * wave; pair0 < pairs; pair0 += kPairs * (kReleaseThreads / 64)) {
+            uint32_t word[kPairs], from[kPairs];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                word[i] = marks[2 * (pair0 + i) + (lane >> 5)];
+                from[i] = places[2 * (pair0 + i) + (lane >> 5)];
+            }
+            uint32_t base = 0;                  // of the wave that had these words
+#pragma unroll
+            for (int i = 0; i < kReleaseThreads / 64; ++i) base = pair0 / 32 == i ? before[i] : base;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const uint32_t bit = lane & 31;
+                if (!(word[i] >> bit & 1u)) continue;
+                const int64_t place = at + base + from[i] + __builtin_popcount(word[i] & ((1u << bit) - 1));
+                const int32_t page = static_cast<int32_t>(w0 * 32 + 64 * (pair0 + i) + lane);
                 a.extra[page] = 0;
                 if (place < a.free_capacity) a.free_pages[place] = page;
-                else full = true;
             }
         }
+        if (bits) __hip_atomic_store(&a.bits[w * kMarkStride], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         at += all;
-        __syncthreads();
     }
-    full = __syncthreads_or(full);
     if (tid == 0) {
-        *a.free_out = static_cast<int32_t>(at < a.free_capacity || !sound ? at : a.free_capacity);
-        const uint32_t pending = __hip_atomic_exchange(&a.ctl->pending, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const bool full = sound && at > a.free_capacity;
+        *a.free_out = static_cast<int32_t>(full ? a.free_capacity : at);
         a.ctl->magic = kSharedMagic;
         a.ctl->flags = (sound ? 0u : kPagedInvalid) | pending | (full ? kPagedCapacity : 0u);
     }

@@ -142,8 +142,10 @@ constexpr int kMaxShared = 1024;        // requests of a fork or release
 
 // Head of the workspace of forks and releases (zero before the first); behind
 // it the places that workgroups count in, 256 bytes apart, 0 between calls,
-// and a bit a page, zero between releases.
-constexpr int kArrivals = 16, kArrivalStride = 64;
+// and a bit a page, zero between releases, 32 of them every kMarkStride words:
+// marks in one line of the cache wait for each other (8000 of 11000 pages given
+// back at once: 15.3 us with the words side by side, 10.6 with a line each).
+constexpr int kArrivals = 16, kArrivalStride = 64, kMarkStride = 16;
 constexpr uint64_t kSharedBits = 256 + 4 * kArrivals * kArrivalStride;
 struct SharedControl {
     uint32_t magic;

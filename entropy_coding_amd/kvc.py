@@ -1026,7 +1026,7 @@ class SharedPages:
             _tensor(t, name, torch.int32, (n,), self.device)
         if free_pages.shape[0] < num_pages:
             raise ValueError(f"free_pages must have room for {num_pages} pages")
-        self._own = _workspace(256 + 4096 + 4 * ((num_pages + 31) // 32), self.device)
+        self._own = _workspace(256 + 4096 + 64 * ((num_pages + 31) // 32), self.device)
         self.workspace = self._own[1]
         self.desc = kvc_shared_pages(free_pages.numel(), _ptr(paged.block_table), _ptr(held), _ptr(self.held_out),
                                      _ptr(free_pages), _ptr(free_count), _ptr(self.free_count_out), _ptr(extra))

@@ -745,7 +745,7 @@ int kvc_paged_compact_result(const void* d_workspace, void* stream);
  */
 #define KVC_MAX_SHARED_REQUESTS 1024
 #define KVC_SHARED_PAGES_WORKSPACE_BYTES(num_pages) \
-    (256u + 4096u + 4u * (((uint64_t)(num_pages) + 31u) / 32u))
+    (256u + 4096u + 64u * (((uint64_t)(num_pages) + 31u) / 32u))
 typedef struct kvc_shared_pages {
     int64_t free_capacity;          /* entries of d_free_pages, < 2^31                */
     int32_t* d_block_table;         /* [batch][max_pages] of h_paged                  */

@@ -119,7 +119,7 @@ def test_compact_refuses_a_short_workspace(kvc):
     assert kvc._lib_compact_result(FAKE + 8, None) == kvc.KVC_ERR_INVALID
 
 
-def shared_status(kvc, fork, ws=FAKE, ws_bytes=256 + 4096 + 4, kv_dtype=0, ch=128, count=3, parents=FAKE, children=FAKE,
+def shared_status(kvc, fork, ws=FAKE, ws_bytes=256 + 4096 + 64, kv_dtype=0, ch=128, count=3, parents=FAKE, children=FAKE,
                   context=FAKE, **kw):
     f = dict(free_capacity=10, d_table=FAKE, d_held_in=FAKE, d_held_out=FAKE, d_free_pages=FAKE, d_free_in=FAKE,
              d_free_out=FAKE, d_extra=FAKE)
@@ -148,7 +148,7 @@ def test_forks_refuse(kvc):
     for bad in (dict(parents=None), dict(parents=FAKE + 2), dict(context=FAKE + 2)):
         assert shared_status(kvc, True, **bad) == kvc.KVC_ERR_INVALID
     for fork in (True, False):
-        assert shared_status(kvc, fork, ws_bytes=256 + 4096 + 3) == kvc.KVC_ERR_CAPACITY
+        assert shared_status(kvc, fork, ws_bytes=256 + 4096 + 63) == kvc.KVC_ERR_CAPACITY
     assert kvc._lib_shared_result(None, None) == kvc.KVC_ERR_INVALID
     assert kvc._lib_shared_result(FAKE + 128, None) == kvc.KVC_ERR_INVALID
 
