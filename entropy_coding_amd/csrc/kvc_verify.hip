@@ -435,8 +435,8 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
                 asm volatile("" ::"v"(done[0]), "v"(done[1]) : "memory");
             }
             if (lane == 0) {
-                place = __hip_atomic_fetch_add(&a.arrived[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                if (place == parts - 1) __hip_atomic_store(&a.arrived[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                place = __hip_atomic_fetch_add(&a.arrived[uint64_t(b) * kArrivedStride], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (place == parts - 1) __hip_atomic_store(&a.arrived[uint64_t(b) * kArrivedStride], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
         }
         __syncthreads();

@@ -634,7 +634,8 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
  * never accepted), or the probabilities that a token is drawn from are all 0
  * (the token is then -1).
  * Workspace: kvc_verify_drafts_sizes (of batch and vocab), 256-byte
- * aligned, all zero before the first call that uses it for this batch.
+ * aligned, all zero before its first call and again before a call of another
+ * batch than the last (its parts lie elsewhere then).
  */
 #define KVC_MAX_DRAFT_NODES 1024
 typedef struct kvc_drafts {
