@@ -20,9 +20,9 @@ constexpr int kAtOnce = 8;                      // rows that a thread reads befo
 // after row: row j goes to place j from a place at or behind it, and places
 // rise, so that what is written was read before by the same thread.  Every
 // workgroup checks its sequence and finds its moves for itself, 64 at a time.
-// Bound by HBM (128 trees, 36 layers, 114 MB: 23.2 us, 4.9 TB/s; 24.9 us with
-// stores that stay in the caches), for small batches by five trips to memory
-// (4.0 us on the GPU).
+// Bound by memory (128 trees, 36 layers, 114 MB: 23.0 us, 4.9 TB/s, 24.9 us with
+// stores that stay in the caches; 31 us where the last-level cache has none of the
+// rows), for small batches by five trips to memory (4.1 us on the GPU).
 __global__ __launch_bounds__(kCompactThreads) void k_compact(CompactArgs a, uint32_t blocks) {
     __shared__ int64_t from[64], to[64];        // slots; from -1: stays
     __shared__ uint32_t moves;
@@ -318,7 +318,10 @@ constexpr int kMerged = 2048;
 // down by itself).  The last workgroup to be done pushes the marked pages in the
 // order of their numbers, clears marks and counts and enters the new state.
 // Bound by its chain of trips to memory: requests, held counts, table, counts,
-// marks, two arrivals, marks (10.6 us, 6.7 for four requests).
+// marks, two arrivals, marks (10.5 us, 6.8 for four requests); in large pools by
+// the last workgroup's way through all the marks, 64 bytes for 32 pages, 1024
+// of them a turn, whatever was released (calls for 4 requests of 63 pages: 7.4 us
+// of 4000 pages, 11.2 of 32768, 21 of 120000, 119 of a million).
 __global__ __launch_bounds__(kReleaseThreads) void k_release(SharedArgs a) {
     __shared__ int32_t requests[kMaxShared], held_by[kMaxShared];
     __shared__ int32_t pages[kMerged], holders[kMerged];

@@ -67,9 +67,10 @@ using Global = __attribute__((address_space(1))) T;     // (a pool's pointer, re
 enum : uint32_t { kQuery, kKey, kValue };
 
 // Two float32 values as e4m3 of x / scale, the scale given as its reciprocal
-// in float64: the product rounded to float32 is the quotient of a bf16 value
-// to the last bit (such a quotient lies further from the middle of two float32
-// values, 2^-49 of itself, than the product is off), and takes a third of the
+// in float64: the product rounded to float32 is the float32 quotient to the
+// last bit (a quotient of two float32 values lies further from the middle of
+// two neighbouring ones, 2^-49 of itself, than the product is off; what is
+// subnormal in float32 is 0 in e4m3 either way), and takes a third of the
 // instructions of a division.
 __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
     const float x = static_cast<float>(double(lo) * per_scale), y = static_cast<float>(double(hi) * per_scale);
@@ -88,7 +89,7 @@ __device__ uint32_t round_scaled(float lo, float hi, double per_scale) {
 // 5.4 TB/s; a copy of as many bytes 82; vector instructions 39% of the cycles),
 // by a wave's trips to memory where they are few (4 rows: 4.0 us on the GPU),
 // by a short launch's start and end between (5003 rows to e4m3, 101 MB: 23 us,
-// a copy's rate gives 21).
+// a copy's rate gives 21; 28 where the last-level cache has none of the rows).
 template <int D, bool FP8, bool NEIGHBOURS, bool UNIFORM>
 __global__ __launch_bounds__(64 * kQkvWaves, 5) void k_qkv(QkvArgs a) {
     constexpr int kUnits = D / 16;              // lanes that a head needs

@@ -59,13 +59,13 @@ struct VerifyLayout {
     uint64_t words, arrived, sums, first_nodes, first_sums, total;
     uint32_t chunks;
 };
-// Words between the sequences' counts: those of one line are added to in turn
-// (64 sequences of 131072 tokens: 20.4 us, with the counts side by side 22.3).
+// Words between the sequences' counts, 64 bytes: counts side by side are added
+// to in turn (64 sequences of 131072 tokens: 20.4 us, side by side 22.3).
 constexpr int kArrivedStride = 16;
 constexpr int kFirsts = 8;              // nodes of a sequence that are summed ahead
 constexpr uint32_t kMostChunks = 64;    // of a workgroup
 // Workgroups of a launch, where it has as many chunks: four a CU (64 sequences
-// of 131072 tokens: 20.5 us, with 512 or 2048 of them 25 and 26).
+// of 131072 tokens: 20.6 us, with 512 or 2048 of them 24.8 and 26.3).
 constexpr uint32_t kDrawGroups = 1024;
 // The workgroups of a sequence, and the chunks of each.
 inline uint32_t verify_parts(uint32_t groups, uint32_t batch, uint32_t chunks, uint32_t* per) {
@@ -145,9 +145,10 @@ constexpr int kMaxShared = 1024;        // requests of a fork or release
 
 // Head of the workspace of forks and releases (zero before the first); behind
 // it the places that workgroups count in, 256 bytes apart, 0 between calls,
-// and a bit a page, zero between releases, 32 of them every kMarkStride words:
-// marks in one line of the cache wait for each other (8000 of 11000 pages given
-// back at once: 15.3 us with the words side by side, 10.6 with a line each).
+// and a bit a page, zero between releases, 32 of them every kMarkStride words,
+// 64 bytes: marks side by side wait for each other (8000 of 11000 pages given
+// back at once: 15.3 us with the words side by side, 10.6 with 64 bytes each).
+// What is read of a pool's marks grows with it: see k_release.
 constexpr int kArrivals = 16, kArrivalStride = 64, kMarkStride = 16;
 constexpr uint64_t kSharedBits = 256 + 4 * kArrivals * kArrivalStride;
 struct SharedControl {

@@ -33,7 +33,9 @@ __device__ float clean(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }
 
 // What is left of probabilities after `rejected` siblings drawn with
 // probabilities q were rejected: each rejection takes q off, and the next
-// sibling meets the rest scaled to a sum of 1 (scales[k], k > 0).
+// sibling meets the rest scaled to a sum of 1 (scales[k], k > 0).  All of them
+// are taken again from the row every time, so that a node's time grows with the
+// square of its rejected siblings.
 template <int N>
 __device__ void reject(float (&y)[N], const float (&q)[N], const float* scales, int rejected) {
     for (int k = 0; k < rejected; ++k) {
@@ -268,8 +270,8 @@ __device__ uint64_t scan_wide(uint64_t x) {
 // and depends on no other node.  (Of a node whose first child is accepted, only
 // that one can be reached.)  All of them are summed over the vocabulary by as
 // many workgroups as the chip takes, so that the walk, which has one CU, need
-// not: 8 trees over 131072 tokens 50 -> 28 us.  Nodes behind the 64th and
-// more than kFirsts of them are left to the walk.
+// not: 8 trees of 12 nodes over 131072 tokens 59 -> 40 us.  Nodes behind
+// the 64th and more than kFirsts of them are left to the walk.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_verify_first(VerifyArgs a, uint32_t parts, uint32_t per) {
     constexpr int kValues = 16;
@@ -331,7 +333,9 @@ __global__ __launch_bounds__(THREADS) void k_verify_first(VerifyArgs a, uint32_t
 // drawn from the draft's probabilities (DRAWN) the sum of what the rejections
 // left is needed before a sibling of a rejected node is tested: a first
 // rejection's may be there (k_verify_first), others are formed by the whole
-// workgroup, bound by what one CU reads (4.6 us for 32000 tokens).
+// workgroup, bound by what one CU reads (4.6 us for 32000 tokens) and, beyond a
+// few siblings, by what it computes: 4 stars of 8, 32 and 64 rejected siblings
+// take 56, 381 and 1244 us over 32000 tokens, 147, 1285 and 4396 over 131072.
 template <int THREADS, bool DRAWN>
 __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts, uint32_t per) {
     constexpr int kWaves = THREADS / 64, kValues = 16;      // of a thread, asked for together
@@ -425,7 +429,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
     }
     if (parts > 1) {
         // The sums first, as exchanges: what they return says that they are done where all dies see them, with no
-        // cache to write back (a release and an acquire of every workgroup took four times as long as all the rest).
+        // cache to write back (with a release and an acquire of every workgroup 64 sequences took 73 us in place of 24).
         if (wave == 0) {
             if (lane < count) {
                 VerifySums* const to = sums + first_chunk + lane;
@@ -518,9 +522,13 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a, uint32_t parts
 // short (16 trees over 32000 tokens: 21 us, with 16 or 256 of them 24 and 23).
 constexpr uint32_t kDrawnGroups = 64, kDrawnGroupsWide = 256;
 // From this many chunks on, first rejections are summed ahead: another launch
-// (1 tree over 32000 tokens 12.4 -> 14.4 us, 200 of them 33 -> 43) that saves a
-// CU's pass over a wide vocabulary (131072 tokens, 1 tree 15.2 -> 14.3 us, 8
-// trees 50 -> 28, 64 of 8 nodes 62 -> 54).
+// that saves a CU's pass over a wide vocabulary.  Without it and with it, us:
+//               1 tree of 8    8 trees of 12    64 of 8
+//    32000 tokens  11.0  13.4     18.9  20.0    29.2  31.2
+//    49152         12.8  14.5     22.3  21.3    37.6  32.7
+//    61441         11.1  13.4     28.4  23.3    51.6  42.8
+//    98304         11.2  13.4     41.7  32.3    70.4  57.7
+//   131072         15.8  14.6     58.8  39.8    95.7  63.8
 constexpr uint32_t kFirstChunks = 16;
 
 }  // namespace

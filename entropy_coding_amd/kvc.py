@@ -1009,7 +1009,9 @@ class SharedPages:
     [num_pages] (0 for pages that one request holds, or none), all int32 and
     the caller's; a call updates them in place, or writes held_out and
     free_count_out where they are given.  A request whose pages were shared
-    ends with release(), not with a trim.  Calls that may run at the same time
+    ends with release(), not with a trim, and is not trimmed below the tokens
+    that it was forked from or with: BlockTable would hand out, without an
+    error, pages that others hold.  Calls that may run at the same time
     need an object each."""
 
     def __init__(self, paged: PagedKV, held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,

@@ -550,9 +550,9 @@ int kvc_paged_attention_result(const void* d_workspace, void* stream);
  * and positive, 1 for bf16 pools).  Of a row whose position is negative
  * nothing is written; of one whose slot is negative or past the pools no key
  * and value.  Two rows of one slot leave a mix of both.  A sum of squares is
- * float32, and float64 where that would overflow; t is formed in float64 and
- * whole turns are taken off there, so that every position has the same
- * precision; all else is float32.
+ * float32, and float64 where that would overflow; t is formed in float64, off
+ * by at most 2^-51 of itself, and whole turns are taken off there, so that far
+ * positions are as exact as near ones; all else is float32.
  * channels 64, 128, 192 or 256; rotary a multiple of 16 from 0 (no rotation:
  * d_frequencies and d_positions may be NULL) to channels; eps at least 1e-30
  * where there is a norm; q_heads 0 (d_q and d_q_out not looked at) to 65536.
@@ -625,8 +625,10 @@ int kvc_paged_qkv(const kvc_paged_kv* h_paged, int64_t layer, const kvc_qkv* p, 
  * as 0; rows of probabilities are taken to sum to 1.  Random numbers lie in
  * [0, 1).
  * vocab and batch at most 2^20, batch x ceil(vocab / 4096) < 2^24; a row
- * stride (in values, at least vocab) between one row is not looked at.  Does
- * not synchronise.
+ * stride (in values, at least vocab) between one row is not looked at.  With
+ * d_draft and d_parents the time grows with the square of the siblings that
+ * are rejected at one node (64 of them over 131072 tokens take 4.4 ms, so a
+ * thousand about a second).  Does not synchronise.
  * kvc_verify_drafts_result gives KVC_ERR_INVALID where a sequence's row starts
  * fall or pass `rows` or it has too many nodes (its kept length is then 0 and
  * nothing else of it written), where a parent does not come before its node
@@ -733,12 +735,16 @@ int kvc_paged_compact_result(const void* d_workspace, void* stream);
  * holders than it has (given back once), or a *d_free_in outside [0,
  * free_capacity] (nothing is done); KVC_ERR_CAPACITY where the stack would
  * pass free_capacity, as one that holds a page twice may (what fits is pushed).
+ * It looks through a mark of every page of the pools, so that large pools take
+ * longer however few pages are released (32768 pages 4 us, a million 110).
  *
  * A request whose pages were shared is finished with kvc_release_pages, not
  * with a trim, and not trimmed below the tokens that it was forked from or
- * with.  d_held_out / d_free_out may be d_held_in / d_free_in, or other
- * arrays.  count at most 1024, at most 2^20 pools, which are 16-byte aligned;
- * free_capacity at least num_pages.  Neither call synchronises;
+ * with: kvc_build_block_table does not know d_extra, and would put pages that
+ * others hold on the stack without an error.  d_held_out / d_free_out may be
+ * d_held_in / d_free_in, or other arrays.  count at most 1024, at most 2^20
+ * pools, which are 16-byte aligned; free_capacity at least num_pages.  Neither
+ * call synchronises;
  * kvc_shared_pages_result gives the outcome of the last one of either kind
  * queued with the workspace.
  * Workspace: KVC_SHARED_PAGES_WORKSPACE_BYTES(num_pages), 256-byte aligned,
